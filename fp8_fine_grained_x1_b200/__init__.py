@@ -13,9 +13,13 @@ Entry points (same names as the C ABI):
   fp8_quant_w_128x128(w, q, sW, scale_mode=SCALE_FP32)
   fp8_blockscaled_gemm(A, sA, B, sB, D, b_major=B_KMAJOR, sb_gran=128)
   fp8_grouped_gemm(A, sA, B, sB, group_offsets, D)
+  fp8_swiglu_quant(h, qa, sa, qh=None, sh=None, n_rows=None)
+  fp8_swiglu_bwd(qh, sh, da, dh=, qdh=, sdh=, qdhT=, sdhT=, qaT=, saT=, n_rows=)
+  fp8_moe_mlp_few(x, topk, weights, W13, s13, W2, s2, out, workspace)
   fp8_get_status(), fp8_set_wait_timeout_ns(ns), fp8_selftest_wait_timeout()
 plus allocating conveniences quant_act_1x128 / quant_act_128x1 / quant_w_128x128
-/ gemm / grouped_gemm that create the output tensors with torch first.
+/ gemm / grouped_gemm / swiglu_quant / swiglu_bwd / moe_mlp_few that create the
+output tensors with torch first.
 """
 from __future__ import annotations
 
@@ -47,8 +51,11 @@ EXPORTED = (
     "fp8_moe_dispatch_workspace_bytes", "fp8_moe_dispatch", "fp8_moe_combine",
     "fp8_moe_dispatch_noalloc", "fp8_requant_1x128_to_128x1", "fp8_blockscaled_gemm_pow2",
     "fp8_grouped_gemm_pow2", "fp8_moe_quant_dispatch", "fp8_selftest_gemm_unwind",
-    "fp8_grouped_gemm_gather", "fp8_moe_route",
+    "fp8_grouped_gemm_gather", "fp8_moe_route", "fp8_swiglu_quant", "fp8_swiglu_bwd",
+    "fp8_moe_mlp_few_workspace_bytes", "fp8_moe_mlp_few",
 )
+
+MOE_FEW_MAX_TOKENS = 128     # FP8_MOE_FEW_MAX_TOKENS
 
 
 class Fp8Error(RuntimeError):
@@ -118,6 +125,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fp8_moe_dispatch_noalloc.restype = _I
     lib.fp8_requant_1x128_to_128x1.argtypes = [_P, _I64, _P, _I64, _I64, _P, _I64, _P, _I, _P]
     lib.fp8_requant_1x128_to_128x1.restype = _I
+    lib.fp8_swiglu_quant.argtypes = [_P, _I, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _P, _P, _I,
+                                     _P]
+    lib.fp8_swiglu_quant.restype = _I
+    lib.fp8_swiglu_bwd.argtypes = [_P, _I64, _P, _P, _I, _I64, _I64, _I64, _P, _I64, _P, _I64, _P,
+                                   _P, _I64, _P, _P, _I64, _P, _P, _I, _P]
+    lib.fp8_swiglu_bwd.restype = _I
+    lib.fp8_moe_mlp_few_workspace_bytes.argtypes = [_I64, _I, _I, _I64, _I64, _I64]
+    lib.fp8_moe_mlp_few_workspace_bytes.restype = _I64
+    lib.fp8_moe_mlp_few.argtypes = [_P, _I, _I64, _I64, _I64, _P, _P, _I, _I, _P, _P, _P, _P, _I64,
+                                    _I64, _P, _I, _I64, _P, _I64, _I, _P]
+    lib.fp8_moe_mlp_few.restype = _I
     _lib = lib
     return lib
 
@@ -314,6 +332,147 @@ def fp8_moe_combine(D, token_row, weights, out, stream=None) -> None:
         _stream(stream)), "fp8_moe_combine")
 
 
+# The gated-MLP calls check their tensors here (dtype, shape, layout, device)
+# before the pointers reach the library, and run on the device of their first
+# input whichever device is current.
+
+def _need(t, name, dtype, shape, device, contiguous=False):
+    """`t` is a device tensor of this dtype and shape with unit stride along its last axis."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be on the CUDA device of the first input ({device}), got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if contiguous:
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    elif t.stride(-1) != 1 and shape[-1] > 1 and t.numel():
+        raise ValueError(f"{name} must have unit stride along its last axis")
+
+
+def _row(t, cols):
+    """Row stride of a 2-D tensor (its width when it has fewer than two rows)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), cols)
+
+
+def _pair(a, b, what):
+    if (a is None) != (b is None):
+        raise ValueError(f"{what} come together: give both or neither")
+    return a is not None
+
+
+def _call_on(device, stream, fn, where, *args):
+    """fn(*args, stream) with `device` current and its current stream unless one is given."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"{where}: stream of {stream.device}, tensors on {device}")
+    if torch.cuda.current_device() == device.index:
+        code = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, stream.cuda_stream)
+    if code != FP8_OK:
+        raise Fp8Error(code, where)
+
+
+def fp8_swiglu_quant(h, qa, sa, qh=None, sh=None, n_rows=None, scale_mode: int = SCALE_FP32,
+                     stream=None) -> None:
+    """h = [gate | up] [M, 2I] bf16/fp32 -> a = silu(gate) * up as 1x128 codes qa [M, I] uint8,
+    scales sa [I/128, M]; with qh [M, 2I] and sh [2I/128, M], also h's own 1x128 codes (the
+    checkpoint fp8_swiglu_bwd reads).  n_rows: int32 device tensor of one element, the number of
+    rows in use (the others are left alone)."""
+    import torch
+    u8, f32 = torch.uint8, torch.float32
+    M, C = h.shape
+    I = C // 2
+    d = h.device
+    _need(h, "h", h.dtype, (M, 2 * I), d)
+    _need(qa, "qa", u8, (M, I), d)
+    _need(sa, "sa", f32, (I // 128, M), d, True)
+    keep = _pair(qh, sh, "qh and sh")
+    if keep:
+        _need(qh, "qh", u8, (M, C), d)
+        _need(sh, "sh", f32, (C // 128, M), d, True)
+    if n_rows is not None:
+        _need(n_rows, "n_rows", torch.int32, (1,), d)
+    _call_on(d, stream, load_library().fp8_swiglu_quant, "fp8_swiglu_quant",
+             _ptr(h), _in_dtype(h), M, I, _row(h, C), _ptr(qa), _row(qa, I), _ptr(sa),
+             _ptr(qh), _row(qh, C) if keep else 0, _ptr(sh), _ptr(n_rows), scale_mode)
+
+
+def fp8_swiglu_bwd(qh, sh, da, dh=None, qdh=None, sdh=None, qdhT=None, sdhT=None, qaT=None,
+                   saT=None, n_rows=None, scale_mode: int = SCALE_FP32, stream=None) -> None:
+    """Backward of the SwiGLU from its checkpoint qh [M, 2I], sh [2I/128, M] and da [M, I]
+    (bf16/fp32).  Any of: dh [M, 2I] bf16; qdh [M, 2I] + sdh [2I/128, M] (1x128); qdhT [2I, M] +
+    sdhT [M/128, 2I] (128x1); qaT [I, M] + saT [M/128, I] (the recomputed activation, 128x1)."""
+    import torch
+    u8, f32 = torch.uint8, torch.float32
+    M, C = qh.shape
+    I = C // 2
+    d = qh.device
+    _need(qh, "qh", u8, (M, 2 * I), d)
+    _need(sh, "sh", f32, (C // 128, M), d, True)
+    _need(da, "da", da.dtype, (M, I), d)
+    if dh is not None:
+        _need(dh, "dh", torch.bfloat16, (M, C), d)
+    rows = _pair(qdh, sdh, "qdh and sdh")
+    if rows:
+        _need(qdh, "qdh", u8, (M, C), d)
+        _need(sdh, "sdh", f32, (C // 128, M), d, True)
+    cols = _pair(qdhT, sdhT, "qdhT and sdhT")
+    if cols:
+        _need(qdhT, "qdhT", u8, (C, M), d)
+        _need(sdhT, "sdhT", f32, (M // 128, C), d, True)
+    act = _pair(qaT, saT, "qaT and saT")
+    if act:
+        _need(qaT, "qaT", u8, (I, M), d)
+        _need(saT, "saT", f32, (M // 128, I), d, True)
+    if n_rows is not None:
+        _need(n_rows, "n_rows", torch.int32, (1,), d)
+    _call_on(d, stream, load_library().fp8_swiglu_bwd, "fp8_swiglu_bwd",
+             _ptr(qh), _row(qh, C), _ptr(sh), _ptr(da), _in_dtype(da), _row(da, I), M, I,
+             _ptr(dh), _row(dh, C) if dh is not None else 0,
+             _ptr(qdh), _row(qdh, C) if rows else 0, _ptr(sdh),
+             _ptr(qdhT), _row(qdhT, M) if cols else 0, _ptr(sdhT),
+             _ptr(qaT), _row(qaT, M) if act else 0, _ptr(saT), _ptr(n_rows), scale_mode)
+
+
+def fp8_moe_mlp_few_workspace_bytes(T: int, k: int, G: int, K: int, I: int, N: int) -> int:
+    return int(load_library().fp8_moe_mlp_few_workspace_bytes(T, k, G, K, I, N))
+
+
+def fp8_moe_mlp_few(x, topk, weights, W13, s13, W2, s2, out, workspace,
+                    scale_mode: int = SCALE_FP32, stream=None) -> None:
+    """A whole MoE MLP for T <= MOE_FEW_MAX_TOKENS tokens: x [T, K] bf16/fp32, topk [T, k] int32,
+    weights [T, k] fp32, W13 [G, 2I, K] and W2 [G, N, I] E4M3 codes with their 128x128 block
+    scales s13 [G, 2I/128, K/128], s2 [G, N/128, I/128] -> out [T, N] bf16/fp32.  workspace:
+    uint8 device tensor of fp8_moe_mlp_few_workspace_bytes(T, k, G, K, I, N) bytes."""
+    import torch
+    u8, f32 = torch.uint8, torch.float32
+    T, K = x.shape
+    k = topk.shape[-1]
+    G, C, _ = W13.shape
+    N = W2.shape[1]
+    I = C // 2
+    d = x.device
+    _need(x, "x", x.dtype, (T, K), d)
+    _need(topk, "topk", torch.int32, (T, k), d, True)
+    _need(weights, "weights", f32, (T, k), d, True)
+    _need(W13, "W13", u8, (G, 2 * I, K), d, True)
+    _need(s13, "s13", f32, (G, C // 128, K // 128), d, True)
+    _need(W2, "W2", u8, (G, N, I), d, True)
+    _need(s2, "s2", f32, (G, N // 128, I // 128), d, True)
+    _need(out, "out", out.dtype, (T, N), d)
+    _need(workspace, "workspace", u8, workspace.shape, d, True)
+    _call_on(d, stream, load_library().fp8_moe_mlp_few, "fp8_moe_mlp_few",
+             _ptr(x), _in_dtype(x), T, K, _row(x, K), _ptr(topk), _ptr(weights), k, G, _ptr(W13),
+             _ptr(s13), _ptr(W2), _ptr(s2), I, N, _ptr(out), _out_dtype(out), _row(out, N),
+             _ptr(workspace), workspace.numel(), scale_mode)
+
+
 def fp8_get_status(stream=None) -> int:
     """Synchronise the stream and return (and clear) the device status word."""
     return load_library().fp8_get_status(_stream(stream))
@@ -421,3 +580,50 @@ def grouped_gemm(A, sA, B, sB, group_offsets, out_dtype=None, stream=None):
     D = torch.empty((A.shape[0], B.shape[1]), dtype=out_dtype or torch.bfloat16, device=A.device)
     fp8_grouped_gemm(A, sA, B, sB, group_offsets, D, stream)
     return D
+
+
+def swiglu_quant(h, keep: bool = True, scale_mode: int = SCALE_FP32, stream=None):
+    """Allocating form of fp8_swiglu_quant: (qa, sa, qh, sh), the last two None without `keep`."""
+    import torch
+    M, C = h.shape
+    u8 = dict(dtype=torch.uint8, device=h.device)
+    f32 = dict(dtype=torch.float32, device=h.device)
+    qa, sa = torch.empty((M, C // 2), **u8), torch.empty((C // 256, M), **f32)
+    qh, sh = ((torch.empty((M, C), **u8), torch.empty((C // 128, M), **f32)) if keep
+              else (None, None))
+    fp8_swiglu_quant(h, qa, sa, qh, sh, None, scale_mode, stream)
+    return qa, sa, qh, sh
+
+
+def swiglu_bwd(qh, sh, da, want=("qdh", "qdhT", "qaT"), scale_mode: int = SCALE_FP32, stream=None):
+    """Allocating form of fp8_swiglu_bwd; `want` names the outputs (dh, qdh, qdhT, qaT), and the
+    dict returned holds them and their scales (sdh, sdhT, saT)."""
+    import torch
+    M, C = qh.shape
+    u8 = dict(dtype=torch.uint8, device=qh.device)
+    f32 = dict(dtype=torch.float32, device=qh.device)
+    out = {}
+    if "dh" in want:
+        out["dh"] = torch.empty((M, C), dtype=torch.bfloat16, device=qh.device)
+    if "qdh" in want:
+        out.update(qdh=torch.empty((M, C), **u8), sdh=torch.empty((C // 128, M), **f32))
+    if "qdhT" in want:
+        out.update(qdhT=torch.empty((C, M), **u8), sdhT=torch.empty((M // 128, C), **f32))
+    if "qaT" in want:
+        out.update(qaT=torch.empty((C // 2, M), **u8), saT=torch.empty((M // 128, C // 2), **f32))
+    fp8_swiglu_bwd(qh, sh, da, **out, scale_mode=scale_mode, stream=stream)
+    return out
+
+
+def moe_mlp_few(x, topk, weights, W13, s13, W2, s2, out_dtype=None, scale_mode: int = SCALE_FP32,
+                stream=None):
+    """Allocating form of fp8_moe_mlp_few."""
+    import torch
+    T, K = x.shape
+    G, C, _ = W13.shape
+    N = W2.shape[1]
+    out = torch.empty((T, N), dtype=out_dtype or torch.bfloat16, device=x.device)
+    n = fp8_moe_mlp_few_workspace_bytes(T, topk.shape[-1], G, K, C // 2, N)
+    ws = torch.empty(max(n, 1), dtype=torch.uint8, device=x.device)
+    fp8_moe_mlp_few(x, topk, weights, W13, s13, W2, s2, out, ws, scale_mode, stream)
+    return out

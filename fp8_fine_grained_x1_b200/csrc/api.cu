@@ -363,12 +363,99 @@ FP8FG_API int fp8_moe_combine(const void* D, int d_dtype, int64_t M_cap, int64_t
                : FP8_ERR_LAUNCH;
 }
 
+FP8FG_API int fp8_swiglu_quant(const void* h, int in_dtype, int64_t M, int64_t I, int64_t ldh,
+                               uint8_t* qa, int64_t ldqa, float* sa, uint8_t* qh, int64_t ldqh,
+                               float* sh, const int32_t* n_rows, int scale_mode, void* stream)
+{
+    if (!is_in(in_dtype) || !is_mode(scale_mode)) return FP8_ERR_DTYPE;
+    if (M < 0 || M > kMaxDim || I <= 0 || I > kMaxDim / 2 || I % 128 || ldh < 2 * I || ldh > kMaxDim ||
+        ldqa < I || ldqa > kMaxDim || (qh && (ldqh < 2 * I || ldqh > kMaxDim)) ||
+        (M + 63) / 64 > kMaxDim / (I / 128))
+        return FP8_ERR_SHAPE;
+    if (M == 0) return FP8_OK;
+    if (!h || !qa || !sa || !qh != !sh) return FP8_ERR_NULL;
+    if (!aligned(h, 16) || !aligned(qa, 16) || !aligned(sa, 4) || !aligned(qh, 16) || !aligned(sh, 4) ||
+        !aligned(n_rows, 4) || (ldh * in_size(in_dtype)) % 16 || ldqa % 16 || (qh && ldqh % 16))
+        return FP8_ERR_ALIGN;
+    if (!device_is_sm100()) return FP8_ERR_DEVICE;
+    return launch_swiglu_quant(h, in_dtype, M, I, ldh, qa, ldqa, sa, qh, ldqh, sh, n_rows, scale_mode,
+                               static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? FP8_OK
+               : FP8_ERR_LAUNCH;
+}
+
+FP8FG_API int fp8_swiglu_bwd(const uint8_t* qh, int64_t ldqh, const float* sh, const void* da,
+                             int in_dtype, int64_t ldda, int64_t M, int64_t I, void* dh, int64_t lddh,
+                             uint8_t* qdh, int64_t ldqdh, float* sdh, uint8_t* qdhT, int64_t ldqdhT,
+                             float* sdhT, uint8_t* qaT, int64_t ldqaT, float* saT,
+                             const int32_t* n_rows, int scale_mode, void* stream)
+{
+    if (!is_in(in_dtype) || !is_mode(scale_mode)) return FP8_ERR_DTYPE;
+    if (M < 0 || M > kMaxDim || I <= 0 || I > kMaxDim / 2 || I % 128 || ldqh < 2 * I || ldqh > kMaxDim ||
+        ldda < I || ldda > kMaxDim || (dh && (lddh < 2 * I || lddh > kMaxDim)) ||
+        (qdh && (ldqdh < 2 * I || ldqdh > kMaxDim)) || (qdhT && (ldqdhT < M || ldqdhT > kMaxDim)) ||
+        (qaT && (ldqaT < M || ldqaT > kMaxDim)) || ((qdhT || qaT) && M % 128) ||
+        (M + 127) / 128 > kMaxDim / (I / 128))
+        return FP8_ERR_SHAPE;
+    if (M == 0) return FP8_OK;
+    if (!qh || !sh || !da || !qdh != !sdh || !qdhT != !sdhT || !qaT != !saT ||
+        (!dh && !qdh && !qdhT && !qaT))
+        return FP8_ERR_NULL;
+    if (!aligned(qh, 16) || !aligned(da, 16) || !aligned(dh, 16) || !aligned(qdh, 16) ||
+        !aligned(qdhT, 16) || !aligned(qaT, 16) || !aligned(sh, 4) || !aligned(sdh, 4) ||
+        !aligned(sdhT, 4) || !aligned(saT, 4) || !aligned(n_rows, 4) || ldqh % 16 ||
+        (ldda * in_size(in_dtype)) % 16 || (dh && lddh % 8) || (qdh && ldqdh % 16) ||
+        (qdhT && ldqdhT % 16) || (qaT && ldqaT % 16))
+        return FP8_ERR_ALIGN;
+    if (!device_is_sm100()) return FP8_ERR_DEVICE;
+    return launch_swiglu_bwd(qh, ldqh, sh, da, in_dtype, ldda, M, I, dh, lddh, qdh, ldqdh, sdh, qdhT,
+                             ldqdhT, sdhT, qaT, ldqaT, saT, n_rows, scale_mode,
+                             static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? FP8_OK
+               : FP8_ERR_LAUNCH;
+}
+
+static bool few_shape_ok(int64_t T, int k, int G, int64_t K, int64_t I, int64_t N)
+{
+    return T >= 0 && T <= FP8_MOE_FEW_MAX_TOKENS && k >= 1 && k <= 1024 && G >= 1 && G <= 1024 && K > 0 &&
+           K <= kMaxDim && K % 128 == 0 && I > 0 && I <= kMaxDim / 2 && I % 128 == 0 && N > 0 &&
+           N <= kMaxDim && N % 128 == 0 && 2 * I <= kMaxDim / G && N <= kMaxDim / G;
+}
+
+FP8FG_API int64_t fp8_moe_mlp_few_workspace_bytes(int64_t T, int k, int G, int64_t K, int64_t I, int64_t N)
+{
+    return few_shape_ok(T, k, G, K, I, N) ? moe_mlp_few_workspace_bytes(T, k, G, K, I, N) : 0;
+}
+
+FP8FG_API int fp8_moe_mlp_few(const void* x, int in_dtype, int64_t T, int64_t K, int64_t ldx,
+                              const int32_t* topk, const float* weights, int k, int G, const uint8_t* W13,
+                              const float* s13, const uint8_t* W2, const float* s2, int64_t I, int64_t N,
+                              void* out, int out_dtype, int64_t ldo, void* workspace,
+                              int64_t workspace_bytes, int scale_mode, void* stream)
+{
+    if (!is_in(in_dtype) || !is_out(out_dtype) || !is_mode(scale_mode)) return FP8_ERR_DTYPE;
+    if (!few_shape_ok(T, k, G, K, I, N) || ldx < K || ldx > kMaxDim || ldo < N || ldo > kMaxDim)
+        return FP8_ERR_SHAPE;
+    if (T == 0) return FP8_OK;
+    if (workspace_bytes < fp8_moe_mlp_few_workspace_bytes(T, k, G, K, I, N)) return FP8_ERR_SHAPE;
+    if (!x || !topk || !weights || !W13 || !s13 || !W2 || !s2 || !out || !workspace) return FP8_ERR_NULL;
+    const int osz = out_dtype == FP8_OUT_BF16 ? 2 : 4;
+    if (!aligned(x, 16) || (ldx * in_size(in_dtype)) % 16 || !aligned(topk, 4) || !aligned(weights, 4) ||
+        !aligned(W13, 16) || !aligned(W2, 16) || !aligned(s13, 4) || !aligned(s2, 4) || !aligned(out, 16) ||
+        (ldo * osz) % 16 || !aligned(workspace, 256))
+        return FP8_ERR_ALIGN;
+    if (!device_is_sm100()) return FP8_ERR_DEVICE;
+    return launch_moe_mlp_few(x, in_dtype, T, K, ldx, topk, weights, k, G, W13, s13, W2, s2, I, N, out,
+                              out_dtype, ldo, workspace, scale_mode, static_cast<cudaStream_t>(stream));
+}
+
 FP8FG_API int fp8_get_status(void* stream)
 {
     const int a = read_and_clear_status(static_cast<cudaStream_t>(stream));
     const int b = read_and_clear_moe_status();
     const int c = read_and_clear_mx_status();
-    return a != FP8_OK ? a : (b != FP8_OK ? b : c);
+    const int d = read_and_clear_few_status();
+    return a != FP8_OK ? a : (b != FP8_OK ? b : (c != FP8_OK ? c : d));
 }
 
 FP8FG_API const char* fp8_status_string(int code)

@@ -27,9 +27,9 @@
  * Conventions shared by every entry point
  *   - Every tensor pointer is caller-owned DEVICE memory on the current CUDA
  *     device (e.g. PyTorch-allocated).  The library allocates nothing and
- *     keeps no per-call state; its only global state is two status words per
- *     device (__device__ variables: one for the GEMM, one for the MoE
- *     dispatch) and a host-side wait time limit.
+ *     keeps no per-call state; its only global state is status words per
+ *     device (__device__ variables, one for each kernel module that reports
+ *     errors) and a host-side wait time limit.
  *   - Per-device set-up (kernel attributes, device addresses of the
  *     library's __device__ arrays) happens at the first call on a device and
  *     is kept for the process; it does not survive cudaDeviceReset().
@@ -356,6 +356,93 @@ int fp8_moe_dispatch_noalloc(const uint8_t* q, const float* sA, int64_t T, int64
  */
 int fp8_moe_combine(const void* D, int d_dtype, int64_t M_cap, int64_t N, const int32_t* token_row,
                     const float* weights, int64_t T, int k, void* out, void* stream);
+
+/*
+ * SwiGLU between the two GEMMs of a gated MLP, quantized for the second one,
+ * with an FP8 checkpoint of its inputs ([P1]/[P2]: 1x128 FP8 tiles cached for
+ * backward; [P5]: FP8 Wgrad lets activations be stored in FP8):
+ *   a[m][i] = silu(h[m][i]) * h[m][I + i],  silu(g) = g / (1 + exp(-g))
+ *   h    [M][ldh] gate columns 0..I-1, then up columns I..2I-1 (the output of
+ *        one GEMM over both), BF16 or FP32
+ *   qa   [M][ldqa] E4M3 codes of a, sa [I/128][M] FP32 scales, in 1x128 groups:
+ *        the A operand of the next GEMM
+ *   qh   [M][ldqh] E4M3 codes of h, sh [2I/128][M]: exactly what
+ *        fp8_quant_act_1x128 writes for h; both NULL when no checkpoint is kept
+ *   n_rows  optional (NULL: M): number of rows in use, one int32 in DEVICE
+ *        memory, e.g. group_offsets + G of a dispatch; clamped to [0, M].  Rows
+ *        at or beyond it are neither read nor written, nor are their scales.
+ * silu and the products are FP32 and a is not rounded before its quantization.
+ * Inputs are finite, and so is a.
+ * Sizes: M >= 0 (0 launches nothing), I > 0, I % 128 == 0, 2I <= 2^31 - 1;
+ * ldh, ldqh >= 2I, ldqa >= I.  n_rows 4-byte aligned.  One kernel launch.
+ */
+int fp8_swiglu_quant(const void* h, int in_dtype, int64_t M, int64_t I, int64_t ldh, uint8_t* qa,
+                     int64_t ldqa, float* sa, uint8_t* qh, int64_t ldqh, float* sh,
+                     const int32_t* n_rows, int scale_mode, void* stream);
+
+/*
+ * Backward of that SwiGLU from the FP8 checkpoint alone ([P1] Figure 6: Dgrad
+ * and Wgrad in FP8; [P2]/[P3]: per-token groups for Dgrad, groups along tokens
+ * for Wgrad).  With g, u = code * scale of the checkpoint and s = 1/(1+exp(-g)):
+ *   dG = dA * u * s * (1 + g * (1 - s)),  dU = dA * g * s,  dH = [dG | dU],
+ *   a  = g * s * u  (recomputed)
+ * Outputs, each one optional (NULL with its scales), at least one wanted:
+ *   dh    [M][lddh] BF16 dH
+ *   qdh   [M][ldqdh] codes of dH in 1x128 groups, sdh [2I/128][M]: the A operand
+ *         of the first GEMM's Dgrad
+ *   qdhT  [2I][ldqdhT] codes of dH in 128x1 groups along tokens, sdhT [M/128][2I]:
+ *         the operand of the first GEMM's Wgrad (as fp8_quant_act_128x1 writes)
+ *   qaT   [I][ldqaT] codes of a in 128x1 groups, saT [M/128][I]: the operand of
+ *         the second GEMM's Wgrad
+ * Every output is rounded once, from the FP32 value.
+ *   qh, sh  the checkpoint (fp8_swiglu_quant), da [M][ldda] BF16 or FP32
+ *   n_rows  as fp8_swiglu_quant.  In the 128x1 groups a row at or beyond it
+ *           counts as zero (code 0 in a group with rows in use); whole groups
+ *           beyond it, and rows of dh and qdh beyond it, are not written.
+ * Sizes: M >= 0, and M % 128 == 0 when qdhT or qaT is wanted; I > 0,
+ * I % 128 == 0, 2I <= 2^31 - 1; ldqh, lddh, ldqdh >= 2I, ldda >= I, ldqdhT,
+ * ldqaT >= M.  One kernel launch.
+ */
+int fp8_swiglu_bwd(const uint8_t* qh, int64_t ldqh, const float* sh, const void* da, int in_dtype,
+                   int64_t ldda, int64_t M, int64_t I, void* dh, int64_t lddh, uint8_t* qdh,
+                   int64_t ldqdh, float* sdh, uint8_t* qdhT, int64_t ldqdhT, float* sdhT,
+                   uint8_t* qaT, int64_t ldqaT, float* saT, const int32_t* n_rows, int scale_mode,
+                   void* stream);
+
+/*
+ * A whole MoE MLP for few tokens ([P4] MoE layer shapes and top-8 routing;
+ * [P5] each group loads one expert's parameters): what quantizing, dispatching,
+ * two grouped GEMMs with the SwiGLU between them and the combine compute, in a
+ * form bound by reading the active experts' weights once instead of by rows
+ * padded to 128 per expert.
+ *   xq = 1x128 codes of x (as fp8_quant_act_1x128); for each expert e picked by
+ *   token t:  h = W13_e . xq[t] (block-scaled, FP32 sums),
+ *   a = 1x128 codes of silu(h[0..I-1]) * h[I..2I-1],  y_e = W2_e . a (FP32);
+ *   out[t] = sum over e of (sum over j with topk[t][j] == e of weights[t][j]) * y_e
+ *   summed in FP32 and rounded once.
+ *   x       [T][ldx] BF16 or FP32 (in_dtype)
+ *   topk    [T][k] int32 expert ids, weights [T][k] FP32 (device memory).  A pair
+ *           whose id is outside [0, G) is dropped and reported as FP8_ERR_SHAPE
+ *           through the status word; an expert named twice by a token counts
+ *           with the sum of its weights; a pair whose weights sum to 0 adds nothing.
+ *   W13     [G][2I][K] E4M3 (gate rows, then up rows), s13 [G][2I/128][K/128]
+ *   W2      [G][N][I] E4M3, s2 [G][N/128][I/128] (as fp8_quant_w_128x128 writes)
+ *   out     [T][ldo] BF16 or FP32 (out_dtype FP8_OUT_*)
+ *   workspace  caller-owned device scratch of fp8_moe_mlp_few_workspace_bytes
+ *           bytes, 256-byte aligned, contents on entry ignored; calls that may
+ *           overlap (other streams, captured graphs that run at once) need one each
+ * The sums are taken in a fixed order: equal inputs give equal bits.
+ * Sizes: 0 <= T <= FP8_MOE_FEW_MAX_TOKENS (0 launches nothing), 1 <= k <= 1024,
+ * 1 <= G <= 1024; K, I, N > 0 and multiples of 128; G*2I, G*N <= 2^31 - 1;
+ * ldx >= K, ldo >= N.  x, W13, W2 and out 16-byte aligned.  Three kernel launches.
+ */
+#define FP8_MOE_FEW_MAX_TOKENS 128
+int64_t fp8_moe_mlp_few_workspace_bytes(int64_t T, int k, int G, int64_t K, int64_t I, int64_t N);
+int fp8_moe_mlp_few(const void* x, int in_dtype, int64_t T, int64_t K, int64_t ldx,
+                    const int32_t* topk, const float* weights, int k, int G, const uint8_t* W13,
+                    const float* s13, const uint8_t* W2, const float* s2, int64_t I, int64_t N,
+                    void* out, int out_dtype, int64_t ldo, void* workspace,
+                    int64_t workspace_bytes, int scale_mode, void* stream);
 
 /*
  * Synchronise `stream`, then return and clear the current device's status
