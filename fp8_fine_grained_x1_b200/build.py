@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libfp8fg.so")
 SOURCES = ["api.cu", "quant.cu", "gemm.cu", "gemm_mx.cu", "moe.cu", "swiglu.cu", "moe_few.cu"]
-HEADERS = ["fp8fg_device.cuh", "fp8fg_quant.cuh", "fp8fg_host.h"]
+HEADERS = ["fp8fg_device.cuh", "fp8fg_quant.cuh", "fp8fg_swiglu.cuh", "fp8fg_host.h"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

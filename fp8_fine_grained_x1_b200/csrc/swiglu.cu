@@ -24,14 +24,11 @@
 #include "fp8fg_device.cuh"
 #include "fp8fg_host.h"
 #include "fp8fg_quant.cuh"
+#include "fp8fg_swiglu.cuh"
 
 namespace fp8fg {
 
 namespace {
-
-// 1 / (1 + exp(-g)).  exp(-g) = inf (g < -88.7) gives 0, whose products
-// with finite values are 0: the limit.
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + expf(-g)); }
 
 // Rows in use: all M, or the device-side count clamped to [0, M].
 __device__ __forceinline__ int64_t live_rows(const int32_t* n_rows, int64_t M)
@@ -41,87 +38,198 @@ __device__ __forceinline__ int64_t live_rows(const int32_t* n_rows, int64_t M)
     return n < 0 ? 0 : (n < M ? n : M);
 }
 
-__device__ __forceinline__ float halfwarp_max(float a)
+// max(|a|, |b|, |c|, |d|)
+__device__ __forceinline__ float absmax4(float a, float b, float c, float d)
 {
-    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 8));
+    return fmaxf(absmax3(a, b, c), fabsf(d));
+}
+
+// Four adjacent elements of a row, as raw bits until they are needed.
+template <typename T>
+struct Quad;
+template <>
+struct Quad<__nv_bfloat16> {
+    uint2 r;
+    __device__ __forceinline__ void zero() { r = make_uint2(0, 0); }
+    __device__ __forceinline__ void load_stream(const __nv_bfloat16* p)
+    {
+        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    }
+    __device__ __forceinline__ void load_shared(const void* p) { r = *static_cast<const uint2*>(p); }
+    __device__ __forceinline__ void get(F2& a, F2& b) const
+    {
+        a = f2(bf16_lo(r.x), bf16_hi(r.x));
+        b = f2(bf16_lo(r.y), bf16_hi(r.y));
+    }
+};
+template <>
+struct Quad<float> {
+    uint4 r;
+    __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void load_stream(const float* p) { r = ld_stream16(p); }
+    __device__ __forceinline__ void load_shared(const void* p) { r = *static_cast<const uint4*>(p); }
+    __device__ __forceinline__ void get(F2& a, F2& b) const
+    {
+        a = f2(__uint_as_float(r.x), __uint_as_float(r.y));
+        b = f2(__uint_as_float(r.z), __uint_as_float(r.w));
+    }
+};
+
+// Four scaled values -> four E4M3 codes (round to nearest even, saturating).
+__device__ __forceinline__ uint32_t cvt4(float a, float b, float c, float d)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
+__device__ __forceinline__ uint32_t scale_cvt4(F2 a, F2 b, float inv)
+{
+    const F2 s = f2(inv, inv), x = a * s, y = b * s;
+    return cvt4(lo(x), hi(x), lo(y), hi(y));
+}
+
+// ------------------------------------------------------------ forward
+
+// Rows per lane, and CTAs per SM (which caps the registers at 80): of 1 and 2 rows with 2 to 5
+// CTAs, 2 and 3 ran fastest (135168 x 2048: 322 us; the others 355 to 419).
+constexpr int kFwdSteps = 2;
+constexpr int kFwdCtasPerSm = 3;
+constexpr int kFwdRowsPerCta = 32 * kFwdSteps;   // 8 warps x 4 rows x steps
+
+// Lane l of a row's 8 lanes owns 16 of a group's 128 channels, in 16-byte pieces 128 bytes
+// apart (so that the 8 lanes of a row read 128 contiguous bytes at a time): BF16 2 pieces of 8
+// channels, FP32 4 of 4.
+template <typename T>
+struct Sixteen;
+template <>
+struct Sixteen<__nv_bfloat16> {
+    static constexpr int kPieces = 2, kPer = 8;
+    uint4 r[2];
+    __device__ __forceinline__ void get(F2 (&v)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            v[4 * i] = f2(bf16_lo(r[i].x), bf16_hi(r[i].x));
+            v[4 * i + 1] = f2(bf16_lo(r[i].y), bf16_hi(r[i].y));
+            v[4 * i + 2] = f2(bf16_lo(r[i].z), bf16_hi(r[i].z));
+            v[4 * i + 3] = f2(bf16_lo(r[i].w), bf16_hi(r[i].w));
+        }
+    }
+    static __device__ __forceinline__ void store(uint8_t* dst, const uint32_t (&c)[4])   // dst: channel 0 + 8 * lane
+    {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[1]);
+        *reinterpret_cast<uint2*>(dst + 64) = make_uint2(c[2], c[3]);
+    }
+};
+template <>
+struct Sixteen<float> {
+    static constexpr int kPieces = 4, kPer = 4;
+    uint4 r[4];
+    __device__ __forceinline__ void get(F2 (&v)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = f2(__uint_as_float(r[i].x), __uint_as_float(r[i].y));
+            v[2 * i + 1] = f2(__uint_as_float(r[i].z), __uint_as_float(r[i].w));
+        }
+    }
+    static __device__ __forceinline__ void store(uint8_t* dst, const uint32_t (&c)[4])   // dst: channel 0 + 4 * lane
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(dst + 32 * i) = c[i];
+    }
+};
+
+__device__ __forceinline__ float absmax16(const F2 (&v)[8])
+{
+    float m = fmaxf(fabsf(lo(v[0])), fabsf(hi(v[0])));
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = absmax3(m, lo(v[i]), hi(v[i]));
+    return m;
+}
+
+// Max over the 8 lanes of a row.
+__device__ __forceinline__ float row_max(float a)
+{
     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 4));
     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
     return fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
 }
 
-__device__ __forceinline__ float warp_max(float a)
+__device__ __forceinline__ void encode16(const F2 (&v)[8], float inv, uint32_t (&c)[4])
 {
-    return halfwarp_max(fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 16)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = scale_cvt4(v[2 * i], v[2 * i + 1], inv);
 }
 
-// ------------------------------------------------------------ forward
-
-constexpr int kFwdRowsPerHalfWarp = 4;
-constexpr int kFwdRowsPerCta = 16 * kFwdRowsPerHalfWarp;   // 64
-
-__device__ __forceinline__ uint2 encode8(const float (&v)[8], float inv)
-{
-    return make_uint2(encode4(v[0], v[1], v[2], v[3], inv), encode4(v[4], v[5], v[6], v[7], inv));
-}
-
-// CTA = 256 threads = 16 half-warps; a half-warp owns the 128 gate and the 128
-// up channels of one block of one row at a time (16 lanes x 8 + 8 elements),
-// so each of the three groups (g, u, a) reduces over 16 lanes.  A thread has
-// the loads of 4 rows (128 B of BF16) in flight before it uses any.
-// Grid (1-D): channel block fastest, then 64-row blocks, so adjacent CTAs read
-// adjacent segments of the same rows.
+// CTA = 256 threads = 8 warps; 8 lanes own the 128 gate and the 128 up channels of one
+// channel block of a row (16 + 16 a lane), so a warp works on 4 rows at once and each
+// of a row's three groups (a, g, u) reduces its max-abs in three shuffles.  Lane 0 of
+// the row then derives the scale of a, lane 1 that of g, lane 2 that of u, in the same
+// instructions: the two correctly rounded divisions of a scale, three times over in
+// all lanes, would cost more than the SwiGLU itself.
+// Grid (1-D): channel block fastest, then row blocks, so adjacent CTAs read adjacent
+// segments of the same rows.
 template <typename Tin, bool KEEP>
-__global__ void __launch_bounds__(256) k_swiglu_quant(
+__global__ void __launch_bounds__(256, kFwdCtasPerSm) k_swiglu_quant(
     const Tin* __restrict__ h, int64_t M, int64_t I, int64_t ldh, uint8_t* __restrict__ qa,
     int64_t ldqa, float* __restrict__ sa, uint8_t* __restrict__ qh, int64_t ldqh,
     float* __restrict__ sh, const int32_t* __restrict__ n_rows, int mode)
 {
-    const int hw = threadIdx.x >> 4;
-    const int l = threadIdx.x & 15;
+    using V = Sixteen<Tin>;
+    const int l = threadIdx.x & 7;
     const int64_t ncb = I / 128;
     const int64_t cb = blockIdx.x % ncb;
-    const int64_t m0 = (int64_t)(blockIdx.x / ncb) * kFwdRowsPerCta;
+    const int64_t m0 = (int64_t)(blockIdx.x / ncb) * kFwdRowsPerCta + (threadIdx.x >> 3);
     const int64_t rows = live_rows(n_rows, M);
-    if (m0 >= rows) return;
-    const int64_t col = cb * 128 + l * 8;
+    const int64_t col = cb * 128 + l * V::kPer;
 
-    Chunk8<Tin> cg[kFwdRowsPerHalfWarp], cu[kFwdRowsPerHalfWarp];
+    V rg[kFwdSteps], ru[kFwdSteps];
 #pragma unroll
-    for (int i = 0; i < kFwdRowsPerHalfWarp; ++i) {
-        const int64_t m = m0 + i * 16 + hw;
-        if (m < rows) {
-            cg[i].load(h + m * ldh + col);
-            cu[i].load(h + m * ldh + I + col);
-        } else {
-            cg[i].zero();
-            cu[i].zero();
+    for (int i = 0; i < kFwdSteps; ++i) {
+        const int64_t m = m0 + 32 * i;
+        const Tin* src = h + (m < rows ? m : 0) * ldh + col;
+#pragma unroll
+        for (int j = 0; j < V::kPieces; ++j) {
+            rg[i].r[j] = ru[i].r[j] = make_uint4(0, 0, 0, 0);
+            if (m < rows) {
+                rg[i].r[j] = ld_stream16(src + 8 * V::kPer * j);
+                ru[i].r[j] = ld_stream16(src + I + 8 * V::kPer * j);
+            }
         }
     }
 #pragma unroll
-    for (int i = 0; i < kFwdRowsPerHalfWarp; ++i) {
-        const int64_t m = m0 + i * 16 + hw;
+    for (int i = 0; i < kFwdSteps; ++i) {
+        const int64_t m = m0 + 32 * i;
         const bool live = m < rows;
-        float g[8], u[8], a[8];
-        cg[i].get(g);
-        cu[i].get(u);
+        F2 g[8], u[8], a[8];
+        rg[i].get(g);
+        ru[i].get(u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] = g[j] * sigmoid(g[j]) * u[j];
-        const GroupScale ga = group_scale(halfwarp_max(absmax8(a)), mode);
-        if (live) {
-            *reinterpret_cast<uint2*>(qa + m * ldqa + col) = encode8(a, ga.inv);
-            if (l == 0) sa[cb * M + m] = ga.s;
-        }
+        for (int j = 0; j < 8; ++j) a[j] = g[j] * sigmoid2(g[j]) * u[j];
+        float mine = row_max(absmax16(a));
         if (KEEP) {
-            const GroupScale gg = group_scale(halfwarp_max(absmax8(g)), mode);
-            const GroupScale gu = group_scale(halfwarp_max(absmax8(u)), mode);
-            if (live) {
-                *reinterpret_cast<uint2*>(qh + m * ldqh + col) = encode8(g, gg.inv);
-                *reinterpret_cast<uint2*>(qh + m * ldqh + I + col) = encode8(u, gu.inv);
-                if (l == 0) {
-                    sh[cb * M + m] = gg.s;
-                    sh[(ncb + cb) * M + m] = gu.s;
-                }
-            }
+            const float mg = row_max(absmax16(g)), mu = row_max(absmax16(u));
+            mine = l == 1 ? mg : (l == 2 ? mu : mine);
+        }
+        const GroupScale gs = group_scale(mine, mode);
+        if (live && l < (KEEP ? 3 : 1))
+            (l == 0 ? sa + cb * M : sh + (l == 1 ? cb : ncb + cb) * M)[m] = gs.s;
+        uint32_t c[4];
+        encode16(a, __shfl_sync(0xffffffffu, gs.inv, 0, 8), c);
+        if (live) V::store(qa + m * ldqa + col, c);
+        if (KEEP) {
+            const float ig = __shfl_sync(0xffffffffu, gs.inv, 1, 8), iu = __shfl_sync(0xffffffffu, gs.inv, 2, 8);
+            uint8_t* dst = qh + m * ldqh + col;
+            encode16(g, ig, c);
+            if (live) V::store(dst, c);
+            encode16(u, iu, c);
+            if (live) V::store(dst + I, c);
         }
     }
 }
@@ -148,162 +256,267 @@ constexpr int kBwdThreads = 512;
 constexpr int kBwdWarps = kBwdThreads / 32;     // 16
 constexpr int kBwdTok = 128 / kBwdWarps;        // 8 tokens per warp
 
+// Inputs of one tile as they lie in shared memory.
+template <typename Tda>
+struct __align__(16) BwdStage {
+    uint8_t g[128 * 128];                       // checkpoint codes of the gate and the up half
+    uint8_t u[128 * 128];
+    Tda da[128 * 128];
+    float sc[2][128];                           // their scales, per token
+};
+
+// FP32 gradients leave room for one stage (97 KB) beside the transposed codes, BF16 ones for two.
+template <typename Tda>
+constexpr int kBwdStages = sizeof(Tda) == 2 ? 2 : 1;
+
+template <typename Tda>
 struct __align__(16) BwdShared {
+    BwdStage<Tda> stage[kBwdStages<Tda>];
     uint8_t outT[3][128 * 128];                 // transposed codes of dG, dU, a
     float part[3][kBwdWarps][128];              // per-warp max-abs of each channel
     float inv[3][128];                          // per-channel encode factors
 };
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+__device__ __forceinline__ uint32_t pack_bf16(F2 v)
 {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo(v), hi(v));
+    return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-template <typename Tda>
-__device__ __forceinline__ void load4(const Tda* p, float (&v)[4]);
-template <>
-__device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[4])
+// 16 (or 4) bytes global -> shared, asynchronously; zeros when `live` is false.
+__device__ __forceinline__ void cp16(void* dst, const void* src, bool live)
 {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
-    v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+                 "r"(live ? 16 : 0)
+                 : "memory");
 }
-template <>
-__device__ __forceinline__ void load4<float>(const float* p, float (&v)[4])
+__device__ __forceinline__ void cp4(void* dst, const void* src, bool live)
 {
-    const float4 w = __ldg(reinterpret_cast<const float4*>(p));
-    v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),
+                 "r"(live ? 4 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// CTA = 512 threads per tile of 128 tokens x 128 channels of I: warp w owns
-// tokens 8w .. 8w+7, lane l channels 4l .. 4l+3, so a warp holds whole 1x128
-// groups (max-abs by shuffles) and the 128x1 groups combine the warps' maxima
-// through shared memory.  dG, dU and a stay in FP32 registers from the one
-// computation to the encodes.  Transposed codes go through shared memory (the
-// 8-byte pieces of a channel's row XOR-swizzled by the channel's lane, two
-// wavefronts per store) and leave as whole 128-byte rows.
+// Persistent CTAs of 512 threads over tiles of 128 tokens x 128 channels of I (channel
+// block fastest), whose inputs arrive by cp.async while the tile before is worked on:
+// into the other of two stages, or, with FP32 gradients, into the only one once its
+// values have moved to registers.
+// Warp w owns tokens 8w .. 8w+7, lane l channels 4l .. 4l+3, so a warp holds whole 1x128
+// groups (one warp reduction each; lane j derives the scale of group j of the warp's
+// 16 once) and the 128x1 groups combine the warps' maxima through shared memory.  dG,
+// dU and a stay in FP32 registers (96 a thread) from the one computation to both
+// encodes.  Transposed codes go through shared memory (the 8-byte pieces of a
+// channel's row XOR-swizzled by the channel's lane: two wavefronts per store) and
+// leave as whole 128-byte rows.
 // Tokens at or beyond the rows in use count as zero in the 128x1 groups.
 template <typename Tda>
 __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p)
 {
     extern __shared__ __align__(16) uint8_t bwd_raw[];
-    BwdShared& s = *reinterpret_cast<BwdShared*>(bwd_raw);
+    BwdShared<Tda>& s = *reinterpret_cast<BwdShared<Tda>*>(bwd_raw);
+    constexpr int NST = kBwdStages<Tda>;
     const int w = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int64_t ncb = p.I / 128;
-    const int64_t cb = blockIdx.x % ncb;
-    const int64_t t0 = (int64_t)(blockIdx.x / ncb) * 128;
     const int64_t rows = live_rows(p.n_rows, p.M);
-    if (t0 >= rows) return;
-    const int64_t col = cb * 128 + 4 * lane;
-    const Tda* da = static_cast<const Tda*>(p.da);
+    const int64_t tiles = (rows + 127) / 128 * ncb;
+    const bool wantH = p.qdhT != nullptr, wantA = p.qaT != nullptr;
 
-    float v[3][kBwdTok][4];       // dG, dU, a
-#pragma unroll
-    for (int i = 0; i < kBwdTok; ++i) {
-        const int64_t t = t0 + w * kBwdTok + i;
-        float g[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
-        if (t < rows) {
-            const uint32_t qg = __ldg(reinterpret_cast<const uint32_t*>(p.qh + t * p.ldqh + col));
-            const uint32_t qu = __ldg(reinterpret_cast<const uint32_t*>(p.qh + t * p.ldqh + p.I + col));
-            const float sg = __ldg(p.sh + cb * p.M + t), su = __ldg(p.sh + (ncb + cb) * p.M + t);
-            load4<Tda>(da + t * p.ldda + col, d);
-            decode4_e4m3(qg, g);
-            decode4_e4m3(qu, u);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                g[k] *= sg;
-                u[k] *= su;
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float sig = sigmoid(g[k]);
-            const float silu = g[k] * sig;
-            v[0][i][k] = d[k] * u[k] * (sig * (1.0f + g[k] * (1.0f - sig)));
-            v[1][i][k] = d[k] * silu;
-            v[2][i][k] = silu * u[k];
-        }
-    }
-
-#pragma unroll
-    for (int i = 0; i < kBwdTok; ++i) {
-        const int64_t t = t0 + w * kBwdTok + i;
-        if (t >= rows) break;                                     // warp-uniform
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int64_t c = x * p.I + col;
-            const float (&r)[4] = v[x][i];
-            if (p.dh)
-                *reinterpret_cast<uint2*>(p.dh + t * p.lddh + c) =
-                    make_uint2(pack_bf16(r[0], r[1]), pack_bf16(r[2], r[3]));
-            if (p.qdh) {
-                const float m = fmaxf(fmaxf(fabsf(r[0]), fabsf(r[1])), fmaxf(fabsf(r[2]), fabsf(r[3])));
-                const GroupScale gs = group_scale(warp_max(m), p.mode);
-                *reinterpret_cast<uint32_t*>(p.qdh + t * p.ldqdh + c) = encode4(r[0], r[1], r[2], r[3], gs.inv);
-                if (lane == 0) p.sdh[(x * ncb + cb) * p.M + t] = gs.s;
-            }
-        }
-    }
-    if (!p.qdhT && !p.qaT) return;
-
-    const bool want[3] = {p.qdhT != nullptr, p.qdhT != nullptr, p.qaT != nullptr};
-#pragma unroll
-    for (int x = 0; x < 3; ++x) {
-        if (!want[x]) continue;
-        float a[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < kBwdTok; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) a[k] = fmaxf(a[k], fabsf(v[x][i][k]));
-        *reinterpret_cast<float4*>(&s.part[x][w][4 * lane]) = make_float4(a[0], a[1], a[2], a[3]);
-    }
-    __syncthreads();
-    const int64_t tb = t0 / 128;
-    if (threadIdx.x < 384) {
-        const int x = threadIdx.x >> 7, c = threadIdx.x & 127;
-        if (want[x]) {
-            float a = s.part[x][0][c];
-#pragma unroll
-            for (int k = 1; k < kBwdWarps; ++k) a = fmaxf(a, s.part[x][k][c]);
-            const GroupScale gs = group_scale(a, p.mode);
-            s.inv[x][c] = gs.inv;
-            if (x < 2)
-                p.sdhT[tb * 2 * p.I + x * p.I + cb * 128 + c] = gs.s;
-            else
-                p.saT[tb * p.I + cb * 128 + c] = gs.s;
-        }
-    }
-    __syncthreads();
-    const int half = (w & 1) ^ ((lane >> 3) & 1);
-#pragma unroll
-    for (int x = 0; x < 3; ++x) {
-        if (!want[x]) continue;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float inv = s.inv[x][4 * lane + k];
-            const uint2 o = make_uint2(encode4(v[x][0][k], v[x][1][k], v[x][2][k], v[x][3][k], inv),
-                                       encode4(v[x][4][k], v[x][5][k], v[x][6][k], v[x][7][k], inv));
-            const int c = 4 * lane + k;
-            *reinterpret_cast<uint2*>(&s.outT[x][c * 128 + (((w >> 1) ^ (lane & 7)) * 16) + half * 8]) = o;
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int x = 0; x < 3; ++x) {
-        if (!want[x]) continue;
+    auto load = [&](int64_t tile, int st) {
+        const int64_t cb = tile % ncb, t0 = tile / ncb * 128;
+        BwdStage<Tda>& d = s.stage[st];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int id = threadIdx.x + kBwdThreads * i;
-            const int c = id >> 3, chunk = id & 7;
-            const int wl = c >> 2;                                // lane that wrote channel c
-            uint4 q = *reinterpret_cast<const uint4*>(&s.outT[x][c * 128 + ((chunk ^ (wl & 7)) * 16)]);
-            if ((wl >> 3) & 1) q = make_uint4(q.z, q.w, q.x, q.y);
-            uint8_t* dst = x < 2 ? p.qdhT + (x * p.I + cb * 128 + c) * p.ldqdhT
-                                 : p.qaT + (cb * 128 + c) * p.ldqaT;
-            *reinterpret_cast<uint4*>(dst + t0 + chunk * 16) = q;
+            const int r = id >> 3, c = (id & 7) * 16;
+            const bool live = t0 + r < rows;
+            const uint8_t* src = p.qh + (live ? t0 + r : 0) * p.ldqh + cb * 128 + c;
+            cp16(d.g + r * 128 + c, src, live);
+            cp16(d.u + r * 128 + c, src + p.I, live);
         }
+        constexpr int kChunk = 16 / (int)sizeof(Tda), kPerRow = 128 / kChunk;
+        const Tda* da = static_cast<const Tda*>(p.da);
+#pragma unroll
+        for (int i = 0; i < 128 * kPerRow / kBwdThreads; ++i) {
+            const int id = threadIdx.x + kBwdThreads * i;
+            const int r = id / kPerRow, c = id % kPerRow * kChunk;
+            const bool live = t0 + r < rows;
+            cp16(d.da + r * 128 + c, da + (live ? t0 + r : 0) * p.ldda + cb * 128 + c, live);
+        }
+        if (threadIdx.x < 256) {
+            const int x = threadIdx.x >> 7, r = threadIdx.x & 127;
+            const bool live = t0 + r < rows;
+            cp4(&d.sc[x][r], p.sh + (x * ncb + cb) * p.M + (live ? t0 + r : 0), live);
+        }
+    };
+
+    int64_t tile = blockIdx.x;
+    if (tile < tiles) load(tile, 0);
+    cp_commit();
+    for (int it = 0; tile < tiles; ++it, tile += gridDim.x) {
+        const int st = NST == 2 ? it & 1 : 0;
+        const int64_t next = tile + gridDim.x;
+        if (NST == 2) {      // its stage was last read two tiles ago
+            if (next < tiles) load(next, st ^ 1);
+            cp_commit();
+            cp_wait<1>();
+        } else {
+            cp_wait<0>();
+        }
+        __syncthreads();
+
+        const int64_t cb = tile % ncb, t0 = tile / ncb * 128;
+        const int64_t col = cb * 128 + 4 * lane;
+        F2 v[3][kBwdTok][2];      // dG, dU, a
+        {
+            const BwdStage<Tda>& d = s.stage[st];
+#pragma unroll
+            for (int i = 0; i < kBwdTok; ++i) {
+                const int r = w * kBwdTok + i;
+                float gf[4], uf[4];
+                decode4_e4m3(*reinterpret_cast<const uint32_t*>(d.g + r * 128 + 4 * lane), gf);
+                decode4_e4m3(*reinterpret_cast<const uint32_t*>(d.u + r * 128 + 4 * lane), uf);
+                Quad<Tda> q;
+                q.load_shared(d.da + r * 128 + 4 * lane);
+                F2 da[2];
+                q.get(da[0], da[1]);
+                const F2 sg = f2(d.sc[0][r], d.sc[0][r]), su = f2(d.sc[1][r], d.sc[1][r]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const F2 g = f2(gf[2 * k], gf[2 * k + 1]) * sg;
+                    const F2 u = f2(uf[2 * k], uf[2 * k + 1]) * su;
+                    const F2 one = f2(1.0f, 1.0f);
+                    const F2 sig = sigmoid2(g), silu = g * sig;
+                    const F2 rest = fma2(sig, f2(-1.0f, -1.0f), one);              // 1 - s
+                    v[0][i][k] = da[k] * u * (sig * fma2(g, rest, one));
+                    v[1][i][k] = da[k] * silu;
+                    v[2][i][k] = silu * u;
+                }
+            }
+        }
+        if (NST == 1) {           // the stage is in registers: fill it again
+            __syncthreads();
+            if (next < tiles) load(next, 0);
+            cp_commit();
+        }
+
+        // per-warp column maxima for the 128x1 groups
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+            if (!(x < 2 ? wantH : wantA)) continue;
+            float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < kBwdTok; i += 2)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    a[2 * k] = absmax3(a[2 * k], lo(v[x][i][k]), lo(v[x][i + 1][k]));
+                    a[2 * k + 1] = absmax3(a[2 * k + 1], hi(v[x][i][k]), hi(v[x][i + 1][k]));
+                }
+            *reinterpret_cast<float4*>(&s.part[x][w][4 * lane]) = make_float4(a[0], a[1], a[2], a[3]);
+        }
+
+        // 1x128 groups and BF16 rows
+        const int64_t tw = t0 + w * kBwdTok;
+        const int nr = rows - tw < kBwdTok ? (int)(rows - tw) : kBwdTok;      // may be <= 0
+        if (p.dh) {
+#pragma unroll
+            for (int i = 0; i < kBwdTok; ++i)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    if (i < nr)
+                        *reinterpret_cast<uint2*>(p.dh + (tw + i) * p.lddh + x * p.I + col) =
+                            make_uint2(pack_bf16(v[x][i][0]), pack_bf16(v[x][i][1]));
+        }
+        if (p.qdh) {
+            float mine = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kBwdTok; ++i)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const F2 (&r)[2] = v[x][i];
+                    const float m = warp_absmax(absmax4(lo(r[0]), hi(r[0]), lo(r[1]), hi(r[1])));
+                    if (lane == 8 * x + i) mine = m;
+                }
+            const GroupScale gs = group_scale(mine, p.mode);
+            if (lane < 16 && (lane & 7) < nr)
+                p.sdh[((lane >> 3) * ncb + cb) * p.M + tw + (lane & 7)] = gs.s;
+#pragma unroll
+            for (int i = 0; i < kBwdTok; ++i)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float inv = __shfl_sync(0xffffffffu, gs.inv, 8 * x + i);
+                    if (i < nr)
+                        *reinterpret_cast<uint32_t*>(p.qdh + (tw + i) * p.ldqdh + x * p.I + col) =
+                            scale_cvt4(v[x][i][0], v[x][i][1], inv);
+                }
+        }
+        if (!wantH && !wantA) {
+            __syncthreads();      // the stage may be filled again
+            continue;
+        }
+
+        __syncthreads();
+        const int64_t tb = t0 / 128;
+        if (threadIdx.x < 384) {
+            const int x = threadIdx.x >> 7, c = threadIdx.x & 127;
+            if (x < 2 ? wantH : wantA) {
+                float a = s.part[x][0][c];
+#pragma unroll
+                for (int k = 1; k < kBwdWarps; ++k) a = fmaxf(a, s.part[x][k][c]);
+                const GroupScale gs = group_scale(a, p.mode);
+                s.inv[x][c] = gs.inv;
+                if (x < 2)
+                    p.sdhT[tb * 2 * p.I + x * p.I + cb * 128 + c] = gs.s;
+                else
+                    p.saT[tb * p.I + cb * 128 + c] = gs.s;
+            }
+        }
+        __syncthreads();
+        const int half = (w & 1) ^ ((lane >> 3) & 1);
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+            if (!(x < 2 ? wantH : wantA)) continue;
+            const float4 i4 = *reinterpret_cast<const float4*>(&s.inv[x][4 * lane]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const F2 inv = k ? f2(i4.z, i4.w) : f2(i4.x, i4.y);
+                F2 e[kBwdTok];
+#pragma unroll
+                for (int i = 0; i < kBwdTok; ++i) e[i] = v[x][i][k] * inv;
+                const int c = 4 * lane + 2 * k;
+                uint8_t* dst = &s.outT[x][c * 128 + (((w >> 1) ^ (lane & 7)) * 16) + half * 8];
+                *reinterpret_cast<uint2*>(dst) = make_uint2(cvt4(lo(e[0]), lo(e[1]), lo(e[2]), lo(e[3])),
+                                                            cvt4(lo(e[4]), lo(e[5]), lo(e[6]), lo(e[7])));
+                *reinterpret_cast<uint2*>(dst + 128) = make_uint2(cvt4(hi(e[0]), hi(e[1]), hi(e[2]), hi(e[3])),
+                                                                  cvt4(hi(e[4]), hi(e[5]), hi(e[6]), hi(e[7])));
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+            if (!(x < 2 ? wantH : wantA)) continue;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int id = threadIdx.x + kBwdThreads * i;
+                const int c = id >> 3, chunk = id & 7;
+                const int wl = c >> 2;                                // lane that wrote channel c
+                uint4 q = *reinterpret_cast<const uint4*>(&s.outT[x][c * 128 + ((chunk ^ (wl & 7)) * 16)]);
+                if ((wl >> 3) & 1) q = make_uint4(q.z, q.w, q.x, q.y);
+                uint8_t* dst = x < 2 ? p.qdhT + (x * p.I + cb * 128 + c) * p.ldqdhT
+                                     : p.qaT + (cb * 128 + c) * p.ldqaT;
+                *reinterpret_cast<uint4*>(dst + t0 + chunk * 16) = q;
+            }
+        }
+        // No barrier here: part, inv and outT are written again only after the next
+        // tile's first, second and third barriers, which follow these reads.
     }
+    cp_wait<0>();
 }
 
 // Once per kernel and device: opt into its dynamic shared memory.
@@ -337,10 +550,12 @@ cudaError_t fwd(const void* h, int64_t M, int64_t I, int64_t ldh, uint8_t* qa, i
 template <typename Tda>
 cudaError_t bwd(const BwdParams& p, cudaStream_t st)
 {
-    static constexpr int kBytes = (int)sizeof(BwdShared);
+    static constexpr int kBytes = (int)sizeof(BwdShared<Tda>);
     const cudaError_t e = allow_smem<k_swiglu_bwd<Tda>>(kBytes);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)((p.M + 127) / 128 * (p.I / 128));
+    const int64_t tiles = (p.M + 127) / 128 * (p.I / 128);
+    const int64_t sms = device_sm_count();
+    const unsigned grid = (unsigned)(tiles < sms ? tiles : sms);
     k_swiglu_bwd<Tda><<<grid, kBwdThreads, kBytes, st>>>(p);
     return cudaGetLastError();
 }
