@@ -451,11 +451,12 @@ FP8FG_API int fp8_moe_mlp_few(const void* x, int in_dtype, int64_t T, int64_t K,
 
 FP8FG_API int fp8_get_status(void* stream)
 {
-    const int a = read_and_clear_status(static_cast<cudaStream_t>(stream));
-    const int b = read_and_clear_moe_status();
-    const int c = read_and_clear_mx_status();
-    const int d = read_and_clear_few_status();
-    return a != FP8_OK ? a : (b != FP8_OK ? b : (c != FP8_OK ? c : d));
+    const int words[] = {read_and_clear_status(static_cast<cudaStream_t>(stream)),   // synchronises
+                         read_and_clear_moe_status(), read_and_clear_mx_status(),
+                         read_and_clear_few_status(), read_and_clear_swiglu_status()};
+    for (int w : words)
+        if (w != FP8_OK) return w;
+    return FP8_OK;
 }
 
 FP8FG_API const char* fp8_status_string(int code)

@@ -99,6 +99,9 @@ cudaError_t launch_swiglu_bwd(const uint8_t* qh, int64_t ldqh, const float* sh, 
                               float* sdhT, uint8_t* qaT, int64_t ldqaT, float* saT,
                               const int32_t* n_rows, int mode, cudaStream_t st);
 
+// Read and clear that module's status word (caller synchronised).
+int read_and_clear_swiglu_status();
+
 // The MoE MLP for few tokens (moe_few.cu); returns an fp8_status code.
 int64_t moe_mlp_few_workspace_bytes(int64_t T, int k, int G, int64_t K, int64_t I, int64_t N);
 int launch_moe_mlp_few(const void* x, int in_dtype, int64_t T, int64_t K, int64_t ldx, const int32_t* topk,

@@ -53,6 +53,20 @@ __device__ __forceinline__ GroupScale group_scale(float amax, int mode)
         g.inv = __uint_as_float(0x7E800000u);          // 2^126
         return g;
     }
+    // Both quotients correctly rounded.  Where nothing can under- or overflow they come from the
+    // correctly rounded reciprocals r of 448 and of amax: q = fl(x * r) is within a unit in the
+    // last place of x / y, the remainder x - q * y is then exact in one FMA, and
+    // fl(q + remainder * r) is the correctly rounded quotient (Markstein's theorem, "Computation
+    // of elementary functions on the IBM RISC System/6000 processor", 1990; compared with
+    // __fdiv_rn for every FP32 value of this range).  About half the instructions of two divisions.
+    if (__float_as_uint(amax) - 0x0F800000u <= 0x60000000u) {      // 2^-96 <= amax <= 2^96
+        constexpr float r448 = 1.0f / 448.0f;
+        const float q = amax * r448;
+        g.s = fmaf(fmaf(-448.0f, q, amax), r448, q);
+        const float r = __frcp_rn(amax), p = 448.0f * r;
+        g.inv = fmaf(fmaf(-amax, p, 448.0f), r, p);
+        return g;
+    }
     g.inv = __fdiv_rn(448.0f, amax);
     g.s = __fdiv_rn(amax, 448.0f);
     return g;

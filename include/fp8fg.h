@@ -370,7 +370,7 @@ int fp8_moe_combine(const void* D, int d_dtype, int64_t M_cap, int64_t N, const 
  *        fp8_quant_act_1x128 writes for h; both NULL when no checkpoint is kept
  *   n_rows  optional (NULL: M): number of rows in use, one int32 in DEVICE
  *        memory, e.g. group_offsets + G of a dispatch; clamped to [0, M].  Rows
- *        at or beyond it are neither read nor written, nor are their scales.
+ *        at or beyond it do not matter and are not written, nor are their scales.
  * silu and the products are FP32 and a is not rounded before its quantization.
  * Inputs are finite, and so is a.
  * Sizes: M >= 0 (0 launches nothing), I > 0, I % 128 == 0, 2I <= 2^31 - 1;
