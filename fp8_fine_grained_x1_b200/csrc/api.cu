@@ -417,7 +417,7 @@ FP8FG_API int fp8_swiglu_bwd(const uint8_t* qh, int64_t ldqh, const float* sh, c
 
 static bool few_shape_ok(int64_t T, int k, int G, int64_t K, int64_t I, int64_t N)
 {
-    return T >= 0 && T <= FP8_MOE_FEW_MAX_TOKENS && k >= 1 && k <= 1024 && G >= 1 && G <= 1024 && K > 0 &&
+    return T >= 0 && T <= FP8_MOE_FEW_MAX_TOKENS && k >= 1 && k <= 128 && G >= 1 && G <= 1024 && K > 0 &&
            K <= kMaxDim && K % 128 == 0 && I > 0 && I <= kMaxDim / 2 && I % 128 == 0 && N > 0 &&
            N <= kMaxDim && N % 128 == 0 && 2 * I <= kMaxDim / G && N <= kMaxDim / G;
 }

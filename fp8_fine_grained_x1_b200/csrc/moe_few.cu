@@ -11,23 +11,30 @@
 // its N columns, and no rows are gathered or padded to 128: every column of an
 // expert's products is a token, whether it was routed to that expert or not.
 // The columns the tensor cores compute in vain cost nothing next to the
-// weight stream, the B operand is the same token matrix for every expert, and
+// weight stream (128 columns: 0.8 us per 32 KB of weights against 0.75 for
+// reading them), the B operand is the same token matrix for every expert, and
 // the combine happens in the accumulator: column t of expert e's second
 // product is promoted with its activation's scale times t's gate weight for e
-// (0 where e was not picked).
+// (0, and zero codes, where e was not picked).
 //
-// Kernels, in stream order:
-//   k_few_prep      codes and scales of x, the list of active experts, the
-//                   gate-weight table [expert][token], zeroed tile counters
-//   k_few_gemm<1>   persistent; tile = 128 gate + 128 up rows of an expert over
-//                   K; ends in SwiGLU + 1x128 quantization of those 128 channels
-//   k_few_gemm<2>   persistent; tile = 256 output columns over all (expert, I)
+// Kernels, in stream order (each starts while the one before drains):
+//   k_few_prep      codes and scales of x, the gate-weight table [expert][token],
+//                   the list of active experts
+//   k_few_gemm<1>   persistent; tile = 128 gate + 128 up rows of an expert over K;
+//                   leaves the sums, or its parts of them, in scratch
+//   k_few_act       adds the parts; SwiGLU and 1x128 quantization
+//   k_few_gemm<2>   persistent; tile = 256 output columns over all (expert, I);
+//                   whole tiles are rounded and stored, parts left in scratch
+//   k_few_out       adds the parts, rounds
 //
 // Both GEMM kernels lay their tiles' K-blocks end to end and give every CTA an
 // equal contiguous range of them (stream-K), so all SMs stream weights for the
-// same time whatever the tile count.  Parts of a tile meet in global scratch:
-// the CTA that finishes a tile last adds them in CTA order (so results do not
-// depend on timing) and runs the tile's epilogue.  No CTA waits for another.
+// same time whatever the tile count.  Parts of a tile are added in CTA order,
+// so results do not depend on timing.  The adding is done by kernels of its own:
+// inside the GEMMs, by the CTA that finished a tile last, it held up that CTA's
+// weight stream (128 tokens: 15 us per tile of phase 1, 35 us per tile of phase
+// 2), and for one token it took as long as the extra launches do.  No CTA waits
+// for another.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -39,6 +46,7 @@
 #include "fp8fg_device.cuh"
 #include "fp8fg_host.h"
 #include "fp8fg_quant.cuh"
+#include "fp8fg_swiglu.cuh"
 
 namespace fp8fg {
 
@@ -51,17 +59,25 @@ constexpr uint32_t W_BYTES = 2 * WBLK_BYTES;    // two row blocks per stage
 constexpr int NUM_PROMO_WARPS = 8;              // warps 0-3: block 0, 4-7: block 1
 constexpr int PROMO_THREADS = 32 * NUM_PROMO_WARPS;
 constexpr int WARP_TMA = 8, WARP_MMA = 9;
-constexpr int NUM_THREADS = PROMO_THREADS + 64;
-constexpr uint32_t RING_BUDGET = 200 * 1024;
+// 128 token columns need more promotion registers than an even split gives: the kernel then
+// launches a third whole warpgroup (TMA, MMA, 2 idle warps), which hands its registers over.
+// (Spilled, the accumulators went through L2 -- shared memory leaves no L1 -- at 3 us per unit.)
+__host__ __device__ constexpr int num_threads(int nb) { return nb > 64 ? 384 : PROMO_THREADS + 64; }
+constexpr uint32_t LAUNCH_REGS = 168, CTRL_REGS = 72, PROMO_REGS = 216;
+static_assert(128 * CTRL_REGS + 256 * PROMO_REGS <= 384 * LAUNCH_REGS, "register split exceeds the launch allocation");
+constexpr int SLOTS = 8;                        // scale slots (at least MAX_STAGES + 2, see FewShared)
 constexpr int MAX_STAGES = 6;
-
+// A CTA takes at least this many units (or a whole tile): fewer would only leave more parts to add.
+constexpr uint32_t MIN_UNITS = 2;
+// Ring bytes: up to 16 tokens leave room for a CTA of each phase on an SM (phase 2's first weights
+// then load while phase 1 drains); more tokens get one CTA with a deeper ring.
+__host__ __device__ constexpr uint32_t ring_budget(int nb) { return (nb <= 16 ? 104 : 216) * 1024; }
 __host__ __device__ constexpr uint32_t stage_bytes(int nb) { return W_BYTES + (uint32_t)nb * BK; }
 __host__ __device__ constexpr int num_stages(int nb)
 {
-    const int n = (int)(RING_BUDGET / stage_bytes(nb));
+    const int n = (int)(ring_budget(nb) / stage_bytes(nb));
     return n < MAX_STAGES ? n : MAX_STAGES;
 }
-__host__ __device__ constexpr uint32_t dyn_smem(int nb) { return 1024 + num_stages(nb) * stage_bytes(nb); }
 
 // ------------------------------------------------------------ workspace
 
@@ -78,15 +94,15 @@ struct Few {
     int out_dtype, mode;
     uint64_t timeout_ns;
     // workspace
-    int32_t* n_act;         // [1]
-    int32_t* act;           // [A] active experts, ascending
+    int32_t* n_act;         // [1] number of active experts,
+    int32_t* act;           // [A] and they, in ascending order
     float* gate;            // [G][Tp] summed gate weight of token t for expert e
-    int32_t* cnt;           // [A * I/128 + ceil(N/256)] parts finished per split tile
-    uint8_t* xq;            // [T][K] codes, xs [K/128][Tp] scales
+    uint8_t* xq;            // [T][K] codes of x, xs [K/128][Tp] their scales
     float* xs;
     uint8_t* aq;            // [A * Tp][I] codes, as [A][I/128][Tp] scales * gate weight
     float* as;
-    float* part;            // [2 * CTAs][2][T][128] partial tiles
+    float* part;            // [2 * CTAs][2][T][128] parts of tiles that several CTAs share
+    float* whole;           // [A * I/128][2][T][128] phase 1's other tiles
 };
 
 int few_tp(int64_t T) { return (int)((T + 15) / 16 * 16); }
@@ -105,75 +121,87 @@ int64_t few_layout(Few* f, uint8_t* base, int64_t T, int k, int G, int64_t K, in
     uint8_t* n_act = take(4);
     uint8_t* act = take(4 * A);
     uint8_t* gate = take(4 * G * Tp);
-    uint8_t* cnt = take(4 * (A * (I / 128) + (N + 255) / 256));
     uint8_t* xq = take(T * K);
     uint8_t* xs = take(4 * (K / 128) * Tp);
     uint8_t* aq = take(A * Tp * I);
     uint8_t* as = take(4 * A * (I / 128) * Tp);
     uint8_t* part = take(4 * 2 * (int64_t)kFewMaxCtas * 2 * T * 128);
+    uint8_t* whole = take(4 * A * (I / 128) * 2 * T * 128);
     if (f) {
         f->n_act = reinterpret_cast<int32_t*>(n_act);
         f->act = reinterpret_cast<int32_t*>(act);
         f->gate = reinterpret_cast<float*>(gate);
-        f->cnt = reinterpret_cast<int32_t*>(cnt);
         f->xq = xq;
         f->xs = reinterpret_cast<float*>(xs);
         f->aq = aq;
         f->as = reinterpret_cast<float*>(as);
         f->part = reinterpret_cast<float*>(part);
+        f->whole = reinterpret_cast<float*>(whole);
     }
     return off;
 }
+
+// Programmatic dependent launch: let the next kernel of the stream start its set-up (and, in
+// k_few_gemm<2>, its weight loads), and wait until the kernel before has completed.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ------------------------------------------------------------ preparation
 
 constexpr int kMaxExperts = 1024;
 
-// Block 0 lists the active experts in ascending order; the others quantize x
-// (a half-warp per 1x128 group, as k_quant_1x128) and share the gate table and
-// the counters' zeroing.
+// The experts some token picked.
+struct ExpertList {
+    int n;
+    uint32_t mask[kMaxExperts / 32];
+    uint16_t id[kMaxExperts];             // in ascending order
+};
+
+// Lists the active experts, by the whole block, from topk.
+__device__ __forceinline__ void list_experts(const Few& f, ExpertList& x)
+{
+    const int tid = threadIdx.x;
+    if (tid < kMaxExperts / 32) x.mask[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < f.T * f.k; i += blockDim.x) {
+        const int32_t e = __ldg(f.topk + i);
+        if (e >= 0 && e < f.G) atomicOr(&x.mask[e >> 5], 1u << (e & 31));
+    }
+    __syncthreads();
+    if (tid < 32) {
+        uint32_t w = x.mask[tid];
+        int incl = __popc(w);
+        const int mine = incl;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, incl, d);
+            if (tid >= d) incl += t;
+        }
+        for (int at = incl - mine; w; w &= w - 1) x.id[at++] = (uint16_t)(tid * 32 + __ffs(w) - 1);
+        if (tid == 31) x.n = incl;
+    }
+    __syncthreads();
+}
+
+// Quantizes x (a half-warp per 1x128 group, as k_quant_1x128), fills the gate table and reports
+// expert ids outside [0, G); the last block lists the active experts.
 template <typename Tin>
 __global__ void __launch_bounds__(256) k_few_prep(const Few f, const Tin* __restrict__ x, int64_t ldx)
 {
     const int tid = threadIdx.x;
-    if (blockIdx.x == 0) {
-        __shared__ int32_t flag[kMaxExperts];
-        __shared__ int32_t wsum[8];
-        for (int e = tid; e < kMaxExperts; e += 256) flag[e] = 0;
-        __syncthreads();
-        for (int64_t i = tid; i < (int64_t)f.T * f.k; i += 256) {
-            const int32_t e = __ldg(f.topk + i);
-            if (e >= 0 && e < f.G)
-                flag[e] = 1;
-            else
-                report_error(FP8_ERR_SHAPE);
-        }
-        __syncthreads();
-        int mine = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mine += flag[4 * tid + i];
-        int incl = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int t = __shfl_up_sync(0xffffffffu, incl, d);
-            if ((tid & 31) >= d) incl += t;
-        }
-        if ((tid & 31) == 31) wsum[tid >> 5] = incl;
-        __syncthreads();
-        int at = incl - mine;
-        for (int wq = 0; wq < (tid >> 5); ++wq) at += wsum[wq];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (flag[4 * tid + i]) f.act[at++] = 4 * tid + i;
-        if (tid == 255) *f.n_act = at;
+    launch_dependents();
+    if (blockIdx.x == gridDim.x - 1) {
+        __shared__ ExpertList experts;
+        list_experts(f, experts);
+        for (int i = tid; i < experts.n; i += 256) f.act[i] = experts.id[i];
+        if (tid == 0) *f.n_act = experts.n;
         return;
     }
-    const int64_t nkb = f.K / 128;
-    const int64_t b = blockIdx.x - 1, nb = gridDim.x - 1;
-    const int64_t grp = b * 16 + (tid >> 4);
+    const uint32_t nkb = (uint32_t)(f.K / 128);
+    const uint32_t grp = blockIdx.x * 16 + (tid >> 4);
     const int l = tid & 15;
-    const bool live = grp < f.T * nkb;
-    const int64_t t = live ? grp / nkb : 0, kb = live ? grp % nkb : 0;
+    const uint32_t t = grp / nkb, kb = grp - t * nkb;
+    const bool live = t < (uint32_t)f.T;
     Chunk8<Tin> c;
     if (live)
         c.load(x + t * ldx + kb * 128 + l * 8);
@@ -188,18 +216,20 @@ __global__ void __launch_bounds__(256) k_few_prep(const Few f, const Tin* __rest
     if (live) {
         *reinterpret_cast<uint2*>(f.xq + t * f.K + kb * 128 + l * 8) =
             make_uint2(encode4(v[0], v[1], v[2], v[3], g.inv), encode4(v[4], v[5], v[6], v[7], g.inv));
-        if (l == 0) f.xs[kb * f.Tp + t] = g.s;
+        if (l == 0) f.xs[(int64_t)kb * f.Tp + t] = g.s;
     }
-    const int64_t A = (int64_t)f.T * f.k < f.G ? (int64_t)f.T * f.k : f.G;
-    const int64_t ncnt = A * (f.I / 128) + (f.N + 255) / 256;
-    for (int64_t i = b * 256 + tid; i < ncnt; i += nb * 256) f.cnt[i] = 0;
-    for (int64_t i = b * 256 + tid; i < (int64_t)f.G * f.Tp; i += nb * 256) {
-        const int e = (int)(i / f.Tp), tt = (int)(i % f.Tp);
+    const int64_t step = ((int64_t)gridDim.x - 1) * 256, i0 = (int64_t)blockIdx.x * 256 + tid;
+    for (int64_t i = i0; i < (int64_t)f.G * f.Tp; i += step) {
+        const int e = (int)((uint32_t)i / (uint32_t)f.Tp), tt = (int)((uint32_t)i % (uint32_t)f.Tp);
         float sum = 0.0f;
         if (tt < f.T)
             for (int j = 0; j < f.k; ++j)
-                if (__ldg(f.topk + (int64_t)tt * f.k + j) == e) sum += __ldg(f.weights + (int64_t)tt * f.k + j);
+                if (__ldg(f.topk + tt * f.k + j) == e) sum += __ldg(f.weights + tt * f.k + j);
         f.gate[i] = sum;
+    }
+    for (int64_t i = i0; i < (int64_t)f.T * f.k; i += step) {
+        const int32_t e = __ldg(f.topk + i);
+        if (e < 0 || e >= f.G) report_error(FP8_ERR_SHAPE);
     }
 }
 
@@ -212,6 +242,24 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* m
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(smem_dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// The same for data that is read once: its L2 lines are the first to go, so that the activations and
+// partial sums written in between stay.
+__device__ __forceinline__ uint64_t policy_evict_first()
+{
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void tma_load_2d_once(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int32_t x,
+                                                 int32_t y, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
 }
 
@@ -233,18 +281,19 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar)
                  : "memory");
 }
 
-__device__ __forceinline__ void promo_sync()   // the promotion warps only
-{
-    asm volatile("bar.sync 1, %0;" ::"n"(PROMO_THREADS) : "memory");
-}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
 
 // ------------------------------------------------------------ GEMM
 
+template <int NB>
 struct __align__(16) FewShared {
-    float vec[NUM_PROMO_WARPS][2][128];   // per-warp token scales, double-buffered
-    float up[16][128];                    // SwiGLU epilogue: up values of 16 tokens
-    float wmax[4][16];                    // its per-warp max-abs
-    uint8_t codes[16][128];               // and its codes
+    // A unit's scales arrive with its operands, in slot (unit number) % 8: the weight scale of
+    // each row block and the tokens' scales.  A slot is refilled 8 units later, when the ring
+    // (at most 6 stages) has been through the MMA of a unit that is at least 6 back, which
+    // waited for the promotion of the unit 2 before that: its readers are done.
+    float tok[SLOTS][NB];
+    float wsc[SLOTS][2];
     uint64_t full[MAX_STAGES];
     uint64_t empty[MAX_STAGES];
     uint64_t tfull[2];
@@ -252,97 +301,202 @@ struct __align__(16) FewShared {
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
-    int last;
+    ExpertList experts;
 };
 
-// The units (tile, K-block) of all tiles end to end, and this CTA's range.
+// The units (tile, K-block) of all tiles end to end, and this CTA's range.  A unit is 32 KB of
+// weights, so unit counts times 152 CTAs fit in 32 bits for any memory.
 struct Range {
-    int64_t U, P, per;      // units, CTAs that have work, units per tile
-    int64_t u0, u1;
-    __device__ __forceinline__ int64_t begin(int64_t c) const { return c * U / P; }
-    __device__ __forceinline__ int64_t owner(int64_t u) const { return ((u + 1) * P - 1) / U; }
+    uint32_t U, P, per;     // units, CTAs that have work, units per tile
+    uint32_t u0, u1;
+    __device__ __forceinline__ uint32_t begin(uint32_t c) const { return c * U / P; }
+    __device__ __forceinline__ uint32_t owner(uint32_t u) const { return ((u + 1) * P - 1) / U; }
 };
 
 template <int PHASE>
-__device__ __forceinline__ Range few_range(const Few& f, int n_act)
+__device__ __forceinline__ Range few_range(const Few& f, int n_act, uint32_t ctas)
 {
     Range r;
-    const int64_t J = f.I / 128;
-    r.per = PHASE == 1 ? f.K / BK : n_act * J;
-    r.U = (PHASE == 1 ? n_act * J : (n_act ? (f.N + 255) / 256 : 0)) * r.per;
-    r.P = r.U < gridDim.x ? r.U : gridDim.x;
+    const uint32_t J = (uint32_t)(f.I / 128);
+    r.per = PHASE == 1 ? (uint32_t)(f.K / BK) : n_act * J;
+    r.U = (PHASE == 1 ? n_act * J : (n_act ? (uint32_t)((f.N + 255) / 256) : 0)) * r.per;
+    const uint32_t tiles = r.per ? r.U / r.per : 0, want = r.U / MIN_UNITS > tiles ? r.U / MIN_UNITS : tiles;
+    r.P = want < ctas ? want : ctas;
     r.u0 = blockIdx.x < r.P ? r.begin(blockIdx.x) : 0;
     r.u1 = blockIdx.x < r.P ? r.begin(blockIdx.x + 1) : 0;
     return r;
 }
 
-// Rows (of the weight map) of the two 128-row blocks of unit kb of a tile.
+// A walk over a range's units without divisions: tile, K-block in the tile, and the (active
+// expert, 128-channel block of I) the unit's weights belong to.
 template <int PHASE>
-__device__ __forceinline__ void few_rows(const Few& f, int64_t tile, int64_t kb, int32_t& r0, int32_t& r1,
-                                         int32_t& xk, int32_t& yk)
-{
-    const int64_t J = f.I / 128;
-    if (PHASE == 1) {
-        const int64_t e = __ldcg(f.act + tile / J), j = tile % J;
-        r0 = (int32_t)(e * 2 * f.I + j * 128);
-        r1 = r0 + (int32_t)f.I;
-        xk = (int32_t)(kb * BK);
-        yk = 0;
-    } else {
-        const int64_t a = kb / J, e = __ldcg(f.act + a);
-        r0 = (int32_t)(e * f.N + tile * 256);
-        r1 = r0 + 128;      // past this expert's rows in an odd last tile: never stored
-        xk = (int32_t)((kb % J) * BK);
-        yk = (int32_t)(a * f.Tp);
+struct Walk {
+    const uint16_t* act;
+    uint32_t J, per, u, tile, kb, a, j;
+    int32_t e;              // active expert a
+    __device__ __forceinline__ Walk(const Few& f, const uint16_t* experts, const Range& r)
+        : act(experts), J((uint32_t)(f.I / 128)), per(r.per), u(r.u0), tile(0), kb(0), a(0), j(0), e(0)
+    {
+        if (r.u0 >= r.u1) return;
+        tile = u / per;
+        kb = u - tile * per;
+        const uint32_t aj = PHASE == 1 ? tile : kb;
+        a = aj / J;
+        j = aj - a * J;
+        e = act[a];
     }
+    __device__ __forceinline__ void next(uint32_t u1)
+    {
+        ++u;
+        ++kb;
+        bool step = PHASE == 2;
+        if (kb == per) {
+            kb = 0;
+            ++tile;
+            step = true;
+        }
+        if (!step) return;
+        if (++j == J) {
+            j = 0;
+            ++a;
+            if (PHASE == 2 && kb == 0) a = 0;
+            if (u < u1) e = act[a];
+        }
+    }
+};
+
+// 16-byte multiples global -> shared, counted on an mbarrier.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
 }
 
+// A tile into L2 only.
+__device__ __forceinline__ void tma_prefetch_l2(const CUtensorMap* map, int32_t x, int32_t y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
+
+// A CTA lets the next kernel start when this many of its units are left to load.
+constexpr uint32_t TRIGGER_UNITS = 4;
+constexpr int PREFETCH_UNITS = 8;
+
+// Run by the whole of a warp: lane 0 arms the stage barrier and issues its TMA and bulk copies,
+// lanes 0 and 1 each copy one row block's weight scale (4 bytes, cp.async) and arrive when it
+// has landed.
 template <int PHASE, int NB>
-__device__ void few_producer(const CUtensorMap* tmW, const CUtensorMap* tmX, const Few& f, const Range& r,
-                             uint8_t* smem, FewShared& sh)
+__device__ void few_producer(const CUtensorMap* tmW, const CUtensorMap* tmX, const CUtensorMap* tmNext,
+                             const Few& f, const Range& r,
+                             uint8_t* smem, FewShared<NB>& sh, int lane)
 {
     constexpr int NS = num_stages(NB);
-    const uint32_t x_bytes = (uint32_t)f.Tp * BK;
-    int64_t it = 0;
-    for (int64_t u = r.u0; u < r.u1; ++u, ++it) {
+    const int64_t J = f.I / 128, nb128 = f.N / 128, nkb = f.K / BK;
+    const uint32_t bytes = W_BYTES + (uint32_t)f.Tp * (BK + 4);
+    const uint64_t once = policy_evict_first();
+    auto weights = [&](const Walk<PHASE>& k, uint32_t it) {
         const int s = (int)(it % NS);
-        if (!mbar_wait(&sh.empty[s], (uint32_t)((it / NS) & 1) ^ 1u, &sh.abort, f.timeout_ns)) break;
-        int32_t r0, r1, xk, yk;
-        few_rows<PHASE>(f, u / r.per, u % r.per, r0, r1, xk, yk);
         uint8_t* dst = smem + s * stage_bytes(NB);
-        mbar_arrive_expect_tx(&sh.full[s], W_BYTES + x_bytes);
-        tma_load_2d(dst, tmW, &sh.full[s], xk, r0);
-        tma_load_2d(dst + WBLK_BYTES, tmW, &sh.full[s], xk, r1);
-        tma_load_2d(dst + W_BYTES, tmX, &sh.full[s], xk, yk);
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&sh.full[s], bytes);
+            // the second block of an odd last output tile lies past this expert's rows: never stored
+            const int32_t r0 = (int32_t)(PHASE == 1 ? k.e * 2 * f.I + k.j * 128 : k.e * f.N + k.tile * 256);
+            const int32_t r1 = PHASE == 1 ? r0 + (int32_t)f.I : r0 + 128;
+            const int32_t x = (int32_t)((PHASE == 1 ? k.kb : k.j) * BK);
+            tma_load_2d_once(dst, tmW, &sh.full[s], x, r0, once);
+            tma_load_2d_once(dst + WBLK_BYTES, tmW, &sh.full[s], x, r1, once);
+        }
+        if (lane < 2) {
+            const int64_t nb = 2 * (int64_t)k.tile + lane;
+            const bool live = PHASE == 1 || nb < nb128;
+            const float* src = PHASE == 1 ? f.s13 + (k.e * 2 * J + lane * J + k.j) * nkb + k.kb
+                                          : f.s2 + (live ? (k.e * nb128 + nb) * J + k.j : 0);
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(&sh.wsc[it % SLOTS][lane])),
+                         "l"(src), "r"(live ? 4 : 0)
+                         : "memory");
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sh.full[s]))
+                         : "memory");
+        }
+        __syncwarp();
+    };
+    auto tokens = [&](const Walk<PHASE>& k, uint32_t it) {
+        const int s = (int)(it % NS);
+        if (lane == 0) {
+            tma_load_2d(smem + s * stage_bytes(NB) + W_BYTES, tmX, &sh.full[s],
+                        (int32_t)((PHASE == 1 ? k.kb : k.j) * BK), PHASE == 1 ? 0 : (int32_t)(k.a * f.Tp));
+            bulk_load(sh.tok[it % SLOTS], (PHASE == 1 ? f.xs : f.as) + (int64_t)k.kb * f.Tp, (uint32_t)f.Tp * 4,
+                      &sh.full[s]);
+        }
+        __syncwarp();
+    };
+    // the ring's first weights do not depend on the kernel before
+    Walk<PHASE> k(f, sh.experts.id, r), ahead = k;
+    uint32_t it = 0, n = 0;
+    // (loops kept rolled: a CTA's first pass through code waits for instruction fetches)
+#pragma unroll 1
+    for (; n < NS && ahead.u < r.u1; ++n, ahead.next(r.u1)) weights(ahead, n);
+    wait_previous();
+    bool triggered = false;
+#pragma unroll 1
+    for (; k.u < r.u1; ++it, k.next(r.u1)) {
+        if (!triggered && r.u1 - k.u <= TRIGGER_UNITS) {
+            launch_dependents();
+            triggered = true;
+        }
+        if (it >= n) {
+            const bool ok = mbar_wait(&sh.empty[it % NS], ((it / NS) & 1) ^ 1u, &sh.abort, f.timeout_ns);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            weights(k, it);
+        }
+        tokens(k, it);
+    }
+    if (!triggered) launch_dependents();
+    if (PHASE == 1 && lane == 0) {
+        // While this kernel's last tiles are finished and the next one starts, HBM would idle: the
+        // weights that this CTA's successor reads behind its ring's first ones go to L2.
+        const Range r2 = few_range<2>(f, sh.experts.n, gridDim.x);
+        Walk<2> w(f, sh.experts.id, r2);
+#pragma unroll 1
+        for (int i = 0; i < PREFETCH_UNITS && w.u < r2.u1; ++i, w.next(r2.u1)) {
+            const int32_t r0 = (int32_t)(w.e * f.N + w.tile * 256);
+            tma_prefetch_l2(tmNext, (int32_t)(w.j * BK), r0);
+            if (w.tile * 256 + 128 < f.N) tma_prefetch_l2(tmNext, (int32_t)(w.j * BK), r0 + 128);
+        }
     }
     // every copy issued lands before the CTA exits
-    for (int s = 0; s < NS; ++s) {
-        const int64_t count = it > s ? (it - s + NS - 1) / NS : 0;
-        if (count) mbar_wait_drain(&sh.full[s], (uint32_t)((count - 1) & 1), f.timeout_ns);
-    }
+    if (lane == 0)
+        for (int s = 0; s < NS; ++s) {
+            const uint32_t count = it > (uint32_t)s ? (it - s + NS - 1) / NS : 0;
+            if (count) mbar_wait_drain(&sh.full[s], (count - 1) & 1, f.timeout_ns);
+        }
 }
 
 template <int NB>
-__device__ void few_mma(const Few& f, const Range& r, uint8_t* smem, FewShared& sh)
+__device__ void few_mma(const Few& f, const Range& r, uint8_t* smem, FewShared<NB>& sh)
 {
     constexpr int NS = num_stages(NB);
     const uint32_t base = smem_u32(smem);
     const uint32_t idesc = idesc_e4m3_f32(128, (uint32_t)f.Tp, 0);
-    int64_t it = 0;
-    for (int64_t u = r.u0; u < r.u1; ++u, ++it) {
+    const uint32_t units = r.u1 - r.u0;
+#pragma unroll 1
+    for (uint32_t it = 0; it < units; ++it) {
         const int s = (int)(it % NS);
-        const uint32_t buf = (uint32_t)(it & 1);
-        if (!mbar_wait(&sh.tempty[buf], (uint32_t)((it >> 1) & 1) ^ 1u, &sh.abort, f.timeout_ns) ||
-            !mbar_wait(&sh.full[s], (uint32_t)((it / NS) & 1), &sh.abort, f.timeout_ns))
+        const uint32_t buf = it & 1;
+        if (!mbar_wait(&sh.tempty[buf], ((it >> 1) & 1) ^ 1u, &sh.abort, f.timeout_ns) ||
+            !mbar_wait(&sh.full[s], (it / NS) & 1, &sh.abort, f.timeout_ns))
             break;
         tc_fence_after();
-        const uint32_t w = base + s * stage_bytes(NB);
+        const uint32_t wa = base + s * stage_bytes(NB);
         const uint32_t d = sh.tmem_base + buf * 2 * NB;
 #pragma unroll
         for (int k = 0; k < BK / 32; ++k) {
-            const uint64_t xd = smem_desc_sw128(w + W_BYTES + k * 32, 16, 1024);
-            mma_f8f6f4(d, smem_desc_sw128(w + k * 32, 16, 1024), xd, idesc, k > 0);
-            mma_f8f6f4(d + NB, smem_desc_sw128(w + WBLK_BYTES + k * 32, 16, 1024), xd, idesc, k > 0);
+            const uint64_t xd = smem_desc_sw128(wa + W_BYTES + k * 32, 16, 1024);
+            mma_f8f6f4(d, smem_desc_sw128(wa + k * 32, 16, 1024), xd, idesc, k > 0);
+            mma_f8f6f4(d + NB, smem_desc_sw128(wa + WBLK_BYTES + k * 32, 16, 1024), xd, idesc, k > 0);
         }
         mma_commit(&sh.empty[s]);
         mma_commit(&sh.tfull[buf]);
@@ -351,236 +505,131 @@ __device__ void few_mma(const Few& f, const Range& r, uint8_t* smem, FewShared& 
     mbar_wait_drain(&sh.drain, 0, f.timeout_ns);
 }
 
-// Sum over the CTAs c0..c1 that hold parts of a tile, in CTA order, of element
-// (blk, t, row): `slot(c)` is where CTA c left its part.
+// The parts of a tile: CTAs c0..c1 hold one each, in slots of `stride` floats [2][T][128].
 struct Parts {
     const float* part;
-    int64_t c0, c1, tile_u0, stride;   // stride: floats per slot
     Range r;
-    __device__ __forceinline__ const float* at(int64_t c) const
+    uint32_t c0, c1, tile_u0;
+    int64_t stride;
+    __device__ __forceinline__ Parts(const Few& f, const Range& range, uint32_t u0)
+        : part(f.part), r(range), c0(range.owner(u0)), c1(range.owner(u0 + range.per - 1)), tile_u0(u0),
+          stride((int64_t)2 * f.T * 128)
+    {
+    }
+    __device__ __forceinline__ const float* at(uint32_t c) const
     {
         // a CTA whose range begins inside the tile left its part in slot 0
         return part + (2 * c + (r.begin(c) >= tile_u0 ? 0 : 1)) * stride;
     }
 };
 
-// One tile's 128 activation channels of expert act[tile / J]: SwiGLU of the
-// summed gate and up rows and 1x128 quantization, 16 tokens at a time.
-// Threads 0-127 hold the gate rows, 128-255 the up rows.
-__device__ __forceinline__ void few_finish_swiglu(const Few& f, const Parts& p, int64_t tile, FewShared& sh,
-                                                  int tid)
+__device__ __forceinline__ void store_out(const Few& f, int t, int64_t n, float v)
 {
-    const int64_t J = f.I / 128, a = tile / J, j = tile % J;
-    const int blk = tid >> 7, row = tid & 127, lane = tid & 31, w4 = (tid >> 5) & 3;
-    const float* gate = f.gate + (int64_t)__ldcg(f.act + a) * f.Tp;
-    for (int t0 = 0; t0 < f.T; t0 += 16) {
-        float v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-        for (int64_t c = p.c0; c <= p.c1; ++c) {
-            const float* src = p.at(c) + (int64_t)blk * f.T * 128 + (int64_t)t0 * 128 + row;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (t0 + i < f.T) v[i] += __ldcg(src + i * 128);
-        }
-        if (blk == 1) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) sh.up[i][row] = v[i];
-        }
-        promo_sync();
-        if (blk == 0) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                // a token not routed to this expert (gate weight 0) becomes a zero row
-                const bool routed = t0 + i < f.T && __ldcg(gate + t0 + i) != 0.0f;
-                const float g = v[i];
-                v[i] = routed ? g * __fdividef(1.0f, 1.0f + expf(-g)) * sh.up[i][row] : 0.0f;
-                float m = fabsf(v[i]);
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-                if (lane == 0) sh.wmax[w4][i] = m;
-            }
-        }
-        promo_sync();
-        if (blk == 0) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float m = fmaxf(fmaxf(sh.wmax[0][i], sh.wmax[1][i]), fmaxf(sh.wmax[2][i], sh.wmax[3][i]));
-                const GroupScale gs = group_scale(m, f.mode);
-                sh.codes[i][row] = (uint8_t)encode4(v[i], 0.f, 0.f, 0.f, gs.inv);
-                if (row == i && t0 + i < f.T)
-                    f.as[(a * J + j) * f.Tp + t0 + i] = gs.s * __ldcg(gate + t0 + i);
-            }
-        }
-        promo_sync();
-        if (tid < 128) {
-            const int i = tid >> 3, c16 = (tid & 7) * 16;
-            if (t0 + i < f.T)
-                *reinterpret_cast<uint4*>(f.aq + (a * f.Tp + t0 + i) * f.I + j * 128 + c16) =
-                    *reinterpret_cast<const uint4*>(&sh.codes[i][c16]);
-        }
-        // No barrier here: sh.up and sh.wmax were last read before the third barrier
-        // (sh.up: the second), and sh.codes is written again only after the next
-        // round's first two, which follow these reads.
-    }
-}
-
-// One tile's 256 output columns: the summed parts, rounded to the output type.
-__device__ __forceinline__ void few_finish_out(const Few& f, const Parts& p, int64_t tile, int tid)
-{
-    const int blk = tid >> 7, row = tid & 127;
-    const int64_t n = tile * 256 + tid;
-    if (n >= f.N) return;
-    for (int t0 = 0; t0 < f.T; t0 += 16) {
-        float v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-        for (int64_t c = p.c0; c <= p.c1; ++c) {
-            const float* src = p.at(c) + (int64_t)blk * f.T * 128 + (int64_t)t0 * 128 + row;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (t0 + i < f.T) v[i] += __ldcg(src + i * 128);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            if (t0 + i >= f.T) break;
-            if (f.out_dtype == FP8_OUT_BF16)
-                static_cast<__nv_bfloat16*>(f.out)[(t0 + i) * f.ldo + n] = __float2bfloat16_rn(v[i]);
-            else
-                static_cast<float*>(f.out)[(t0 + i) * f.ldo + n] = v[i];
-        }
-    }
+    if (f.out_dtype == FP8_OUT_BF16)
+        static_cast<__nv_bfloat16*>(f.out)[t * f.ldo + n] = __float2bfloat16_rn(v);
+    else
+        static_cast<float*>(f.out)[t * f.ldo + n] = v;
 }
 
 template <int PHASE, int NB>
-__device__ void few_promotion(const Few& f, const Range& r, FewShared& sh)
+__device__ void few_promotion(const Few& f, const Range& r, FewShared<NB>& sh)
 {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int blk = warp >> 2, row = tid & 127;
     const uint32_t tmem = sh.tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + blk * NB;
-    const int64_t J = f.I / 128, nb128 = f.N / 128;
-    const int64_t slot_floats = (int64_t)2 * f.T * 128;
-    int64_t it = 0;
+    uint32_t it = 0;
     int seg = 0;
-    // Once a wait has run out the warp takes no further part in the work, but
-    // still meets the others at every segment's barriers.
-    bool ok = true;
-    for (int64_t u = r.u0; u < r.u1; ++seg) {
-        const int64_t tile = u / r.per, tile_u0 = tile * r.per;
-        const int64_t end = r.u1 < tile_u0 + r.per ? r.u1 : tile_u0 + r.per;
+    wait_previous();
+    Walk<PHASE> k(f, sh.experts.id, r);
+    for (; k.u < r.u1; ++seg) {
+        const uint32_t tile = k.tile, tile_u0 = k.u - k.kb;
+        // phase 1: the gate weights for the tile's expert (lane l: tokens l, l + 32, ...), and which
+        // tokens were routed to it (weight not 0): only their columns matter
+        constexpr int NW = (NB + 31) / 32;
+        float gw[NW];
+        uint32_t routed[NW];
+        if (PHASE == 1) {
+#pragma unroll
+            for (int i = 0; i < NW; ++i) {
+                const int t = 32 * i + lane;
+                gw[i] = t < f.T ? __ldcg(f.gate + (int64_t)k.e * f.Tp + t) : 0.0f;
+                routed[i] = __ballot_sync(0xffffffffu, gw[i] != 0.0f);
+            }
+        }
+        const uint32_t end = r.u1 < tile_u0 + r.per ? r.u1 : tile_u0 + r.per;
         float acc[NB];
 #pragma unroll
         for (int i = 0; i < NB; ++i) acc[i] = 0.0f;
-        // this K-block's weight-block scale and token scales
-        auto wscale = [&](int64_t uu) -> float {
-            const int64_t kb = uu - tile_u0;
-            if (PHASE == 1) {
-                const int64_t e = __ldcg(f.act + tile / J), j = tile % J;
-                return __ldg(f.s13 + (e * 2 * J + blk * J + j) * (f.K / BK) + kb);
-            }
-            const int64_t e = __ldcg(f.act + kb / J), nb = tile * 2 + blk;
-            return nb < nb128 ? __ldg(f.s2 + (e * nb128 + nb) * J + kb % J) : 0.0f;
-        };
-        auto tscale = [&](int64_t uu) -> float4 {
-            const float* v = (PHASE == 1 ? f.xs : f.as) + (uu - tile_u0) * f.Tp + 4 * lane;
-            return 4 * lane < f.Tp ? __ldcg(reinterpret_cast<const float4*>(v)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        };
-        float sw = wscale(u);
-        *reinterpret_cast<float4*>(&sh.vec[warp][it & 1][4 * lane]) = tscale(u);
-        __syncwarp();
-        for (; ok && u < end; ++u, ++it) {
-            float sw_next = 0.0f;
-            float4 ts_next = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (u + 1 < end) {
-                sw_next = wscale(u + 1);
-                ts_next = tscale(u + 1);
-            }
-            const uint32_t buf = (uint32_t)(it & 1);
+#pragma unroll 1
+        for (; k.u < end; k.next(r.u1), ++it) {
+            const uint32_t buf = it & 1;
             // the whole warp goes on or gives up (TMEM loads are warp-wide)
-            ok = __all_sync(0xffffffffu,
-                            mbar_wait(&sh.tfull[buf], (uint32_t)((it >> 1) & 1), &sh.abort, f.timeout_ns));
-            if (!ok) break;
+            if (!__all_sync(0xffffffffu, mbar_wait(&sh.tfull[buf], (it >> 1) & 1, &sh.abort, f.timeout_ns))) return;
             tc_fence_after();
-            const float* vec = sh.vec[warp][it & 1];
+            const float* vec = sh.tok[it % SLOTS];
+            const float sw = sh.wsc[it % SLOTS][blk];
+            const uint32_t t = tmem + buf * 2 * NB;
+            // CH columns per TMEM round trip (about 200 cycles whatever their number), the next chunk's
+            // in flight while this one's are scaled and added
+            constexpr int CH = NB < 32 ? NB : 32;
+            uint32_t pa[CH], pb[CH];
+            tmem_ld(t, pa);
 #pragma unroll
-            for (int c = 0; c < NB; c += 16) {
+            for (int c = 0; c < NB; c += CH) {
                 if (c >= f.Tp) break;
-                uint32_t p[16];
-                tmem_ld16(tmem + buf * 2 * NB + c, p);
-                float s[16];
-#pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const float4 q = *reinterpret_cast<const float4*>(vec + c + i);
-                    fmul2(s[i], s[i + 1], q.x, q.y, sw, sw);
-                    fmul2(s[i + 2], s[i + 3], q.z, q.w, sw, sw);
-                }
+                uint32_t (&p)[CH] = (c & CH) ? pb : pa;
+                uint32_t (&q)[CH] = (c & CH) ? pa : pb;
                 tmem_ld_wait(p);
+                if (c + CH < NB && c + CH < f.Tp) tmem_ld(t + c + CH, q);
 #pragma unroll
-                for (int i = 0; i < 16; i += 2)
-                    ffma2(acc[c + i], acc[c + i + 1], __uint_as_float(p[i]), __uint_as_float(p[i + 1]), s[i],
-                          s[i + 1]);
+                for (int i = 0; i < CH; i += 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(vec + c + i);
+                    float s0, s1, s2, s3;
+                    fmul2(s0, s1, x.x, x.y, sw, sw);
+                    fmul2(s2, s3, x.z, x.w, sw, sw);
+                    ffma2(acc[c + i], acc[c + i + 1], __uint_as_float(p[i]), __uint_as_float(p[i + 1]), s0, s1);
+                    ffma2(acc[c + i + 2], acc[c + i + 3], __uint_as_float(p[i + 2]), __uint_as_float(p[i + 3]), s2, s3);
+                }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.tempty[buf]);
-            sw = sw_next;
-            *reinterpret_cast<float4*>(&sh.vec[warp][(it + 1) & 1][4 * lane]) = ts_next;
-            __syncwarp();
         }
-        u = end;
 
-        // this CTA's part of the tile, then (for the last CTA to get here) the tile
-        float* dst = f.part + (2 * (int64_t)blockIdx.x + (seg ? 1 : 0)) * slot_floats +
-                     (int64_t)blk * f.T * 128 + row;
+        // The sums, or this CTA's part of them: for k_few_act (phase 1), for k_few_out, or done.
+        const Parts p(f, r, tile_u0);
+        const bool shared = p.c1 > p.c0;
+        if (PHASE == 1 || shared) {
+            float* dst = (shared ? f.part + (2 * (int64_t)blockIdx.x + (seg ? 1 : 0)) * p.stride
+                                 : f.whole + (int64_t)tile * p.stride) +
+                         (int64_t)blk * f.T * 128 + row;
 #pragma unroll
-        for (int t = 0; t < NB; ++t)
-            if (t < f.T) __stcg(dst + t * 128, acc[t]);
-        Parts p;
-        p.part = f.part;
-        p.r = r;
-        p.tile_u0 = tile_u0;
-        p.stride = slot_floats;
-        p.c0 = r.owner(tile_u0);
-        p.c1 = r.owner(tile_u0 + r.per - 1);
-        __threadfence();
-        promo_sync();
-        if (tid == 0) {
-            int last = !*static_cast<volatile int*>(&sh.abort);   // a tile with a missing part is never finished
-            if (last && p.c1 > p.c0) {
-                int32_t* cnt = f.cnt + (PHASE == 1 ? tile
-                                                   : ((int64_t)f.T * f.k < f.G ? (int64_t)f.T * f.k : f.G) * J + tile);
-                last = atomicAdd(cnt, 1) == (int)(p.c1 - p.c0);
-            }
-            sh.last = last;
-            __threadfence();
+            for (int t = 0; t < NB; ++t)
+                if (PHASE == 1 ? (routed[t >> 5] >> (t & 31)) & 1 : t < f.T) __stcg(dst + t * 128, acc[t]);
+        } else if (tile * 256 + (int64_t)tid < f.N) {
+#pragma unroll
+            for (int t = 0; t < NB; ++t)
+                if (t < f.T) store_out(f, t, tile * 256 + (int64_t)tid, acc[t]);
         }
-        promo_sync();
-        if (sh.last) {
-            if (PHASE == 1)
-                few_finish_swiglu(f, p, tile, sh, tid);
-            else
-                few_finish_out(f, p, tile, tid);
-        }
-        promo_sync();     // slot 1 and sh.last are reused by the next segment
     }
 }
 
 template <int PHASE, int NB>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
-    k_few_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Few f)
+__global__ void __launch_bounds__(num_threads(NB), NB <= 16 ? 2 : 1)
+    k_few_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+               const __grid_constant__ CUtensorMap tmNext, const Few f)
 {
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ FewShared sh;
+    // the ring first: its tiles need 1024-byte alignment (128-byte swizzle atoms)
+    extern __shared__ __align__(1024) uint8_t smem[];
     constexpr int NS = num_stages(NB);
+    FewShared<NB>& sh = *reinterpret_cast<FewShared<NB>*>(smem + NS * stage_bytes(NB));
     constexpr uint32_t TMEM_COLS = 4 * NB;     // two buffers of two blocks' NB columns
-    static_assert(TMEM_COLS >= 32 && TMEM_COLS <= 512 && NS >= 2, "TMEM columns and ring depth");
-    const uint32_t raw = smem_u32(smem_raw);
-    uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    static_assert(TMEM_COLS >= 32 && TMEM_COLS <= 512 && NS >= 2 && NS + 2 <= SLOTS, "TMEM columns, ring depth");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.full[s], 3);     // lane 0's bytes, two scales
             mbar_init(&sh.empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -604,26 +653,29 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncthreads();
     tc_fence_after();
 
-    const int n_act = __ldcg(f.n_act);
-    const Range r = few_range<PHASE>(f, n_act);
-    if (warp == WARP_TMA) {
-        if (lane == 0) few_producer<PHASE, NB>(&tmW, &tmX, f, r, smem, sh);
-        __syncwarp();
-    } else if (warp == WARP_MMA) {
-        if (lane == 0) few_mma<NB>(f, r, smem, sh);
+    // Phase 1 lists the active experts itself, so that its first weights can be on their way while
+    // k_few_prep still runs.  Phase 2 reads the list: phase 1 let the kernels behind it start only after
+    // it had seen k_few_prep complete.
+    if (PHASE == 1) {
+        list_experts(f, sh.experts);
+    } else {
+        const int A = f.T * f.k < f.G ? f.T * f.k : f.G;
+        if (threadIdx.x == 0) sh.experts.n = __ldcg(f.n_act);
+        for (int i = threadIdx.x; i < A; i += blockDim.x) sh.experts.id[i] = (uint16_t)__ldcg(f.act + i);
+        __syncthreads();
+    }
+    const Range r = few_range<PHASE>(f, sh.experts.n, gridDim.x);
+    if (warp >= NUM_PROMO_WARPS) {
+        if (num_threads(NB) == 384) regs_dec<CTRL_REGS>();
+        if (warp == WARP_TMA) {
+            few_producer<PHASE, NB>(&tmW, &tmX, &tmNext, f, r, smem, sh, lane);
+        } else if (warp == WARP_MMA && lane == 0) {
+            few_mma<NB>(f, r, smem, sh);
+        }
         __syncwarp();
     } else {
+        if (num_threads(NB) == 384) regs_inc<PROMO_REGS>();
         few_promotion<PHASE, NB>(f, r, sh);
-        if (PHASE == 2 && n_act == 0) {      // no valid expert at all: the sum over none
-            for (int64_t i = (int64_t)blockIdx.x * PROMO_THREADS + threadIdx.x; i < f.T * f.N;
-                 i += (int64_t)gridDim.x * PROMO_THREADS) {
-                const int64_t at = i / f.N * f.ldo + i % f.N;
-                if (f.out_dtype == FP8_OUT_BF16)
-                    static_cast<__nv_bfloat16*>(f.out)[at] = __float2bfloat16_rn(0.0f);
-                else
-                    static_cast<float*>(f.out)[at] = 0.0f;
-            }
-        }
     }
     tc_fence_before();
     __syncthreads();
@@ -632,6 +684,143 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem_base),
                      "r"(TMEM_COLS)
                      : "memory");
+}
+
+// Block (tile of phase 1, 32 tokens): adds the tile's parts for the tokens routed to its expert, 8 at
+// a time, thread = channel; SwiGLU and 1x128 quantization.  Tokens not routed here (gate weight 0)
+// get zero rows of scale 0.  Everything but the parts is known (k_few_prep had completed before phase 1
+// let this kernel start), and done, before phase 1 ends.
+constexpr int ACT_TOKENS = 8;
+
+__global__ void __launch_bounds__(128) k_few_act(const Few f, uint32_t ctas)
+{
+    __shared__ float wmax[4][ACT_TOKENS];
+    __shared__ __align__(16) uint8_t codes[ACT_TOKENS][128];
+    __shared__ uint8_t tcol[32];
+    const int tid = threadIdx.x, lane = tid & 31, w4 = tid >> 5;
+    launch_dependents();
+    const uint32_t J = (uint32_t)(f.I / 128), tile = blockIdx.x, a = tile / J, j = tile - a * J;
+    const int n_act = __ldcg(f.n_act), t0 = 32 * blockIdx.y;
+    const bool live = (int)a < n_act;
+    float gw = 0.0f;                          // gate weight of token t0 + lane
+    if (live && t0 + lane < f.T) gw = __ldcg(f.gate + (int64_t)__ldcg(f.act + a) * f.Tp + t0 + lane);
+    const uint32_t routed = __ballot_sync(0xffffffffu, gw != 0.0f);
+    if (tid < 32 && gw != 0.0f) tcol[__popc(routed & ((1u << lane) - 1))] = (uint8_t)lane;
+    const int n = __popc(routed);
+    const Range r = few_range<1>(f, live ? n_act : 1, ctas);
+    const Parts p(f, r, (live ? tile : 0) * r.per);
+    __syncthreads();
+    if (!live) {
+        wait_previous();
+        return;
+    }
+    const int64_t row0 = (int64_t)a * f.Tp + t0;                     // of aq
+    float* const as = f.as + (int64_t)tile * f.Tp + t0;
+    uint8_t* const aq = f.aq + row0 * f.I + j * 128;
+    const int i8 = lane & (ACT_TOKENS - 1);
+    // A rehearsal of one round while phase 1 still runs, on numbers that are not used, fetches the
+    // instructions: cold, they took longer (3.5 us) than the loads.  (The compiler must not know the
+    // first round's number: it would peel that round off, into code of its own.)
+    int round = -1;
+    asm volatile("" : "+r"(round));
+#pragma unroll 1
+    for (; round * ACT_TOKENS < n; ++round) {
+        const bool real = round >= 0;
+        const int c = real ? round * ACT_TOKENS : 0;
+        if (round == 0) wait_previous();
+        float g[ACT_TOKENS], u[ACT_TOKENS];
+#pragma unroll
+        for (int i = 0; i < ACT_TOKENS; ++i) g[i] = u[i] = 0.0f;
+#pragma unroll 1
+        for (uint32_t q = p.c0; q <= p.c1; ++q) {
+            int now = round;                  // (hidden again: no second copy of this loop either)
+            asm volatile("" : "+r"(now));
+            const float* src = (p.c0 == p.c1 ? f.whole + (int64_t)tile * p.stride : p.at(q)) + (int64_t)t0 * 128 + tid;
+            if (now < 0) src = f.gate;
+            const int64_t up = now < 0 ? 0 : (int64_t)f.T * 128;
+            const int mul = now < 0 ? 0 : 128;
+            float x[2][ACT_TOKENS];           // all in flight at once; past the last column, one not used
+#pragma unroll
+            for (int i = 0; i < ACT_TOKENS; ++i) {
+                const float* col = src + tcol[c + i < n ? c + i : 0] * mul;
+                x[0][i] = __ldcg(col);
+                x[1][i] = __ldcg(col + up);
+            }
+#pragma unroll
+            for (int i = 0; i < ACT_TOKENS; ++i) {
+                g[i] += x[0][i];
+                u[i] += x[1][i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < ACT_TOKENS; ++i)
+            g[i] = g[i] * rcp_approx(1.0f + ex2_approx(g[i] * -1.4426950408889634f)) * u[i];
+#pragma unroll
+        for (int i = 0; i < ACT_TOKENS; ++i) {
+            const float m = warp_absmax(g[i]);
+            if (lane == 0) wmax[w4][i] = m;
+        }
+        __syncthreads();
+        // lane i derives the scale of column c + i
+        const GroupScale gs =
+            group_scale(fmaxf(fmaxf(wmax[0][i8], wmax[1][i8]), fmaxf(wmax[2][i8], wmax[3][i8])), f.mode);
+        const int t = c + i8 < n ? tcol[c + i8] : 0;
+        const float wt = __shfl_sync(0xffffffffu, gw, t);
+        if (real && tid < ACT_TOKENS && c + i8 < n) as[t] = gs.s * wt;
+#pragma unroll
+        for (int k = 0; k < ACT_TOKENS; ++k)
+            codes[k][tid] = (uint8_t)encode4(g[k], 0.f, 0.f, 0.f, __shfl_sync(0xffffffffu, gs.inv, k));
+        __syncthreads();
+        if (real && tid < ACT_TOKENS * 8 && c + (tid >> 3) < n)
+            *reinterpret_cast<uint4*>(aq + (int64_t)tcol[c + (tid >> 3)] * f.I + (tid & 7) * 16) =
+                *reinterpret_cast<const uint4*>(&codes[tid >> 3][(tid & 7) * 16]);
+        // (the next round's writes of codes follow a barrier that these reads precede)
+    }
+    if (n == 0) wait_previous();
+    if (tid < 32 && t0 + lane < f.T && gw == 0.0f) as[lane] = 0.0f;
+    for (int i = tid; i < 32 * 8; i += 128)
+        if (t0 + (i >> 3) < f.T && !((routed >> (i >> 3)) & 1))
+            *reinterpret_cast<uint4*>(aq + (int64_t)(i >> 3) * f.I + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// Output columns whose sums are in parts (the whole tiles are written already): block =
+// 256 columns x OUT_TOKENS tokens, a thread one column, with the loads of OUT_PARTS parts in flight
+// at once.  With no valid expert at all, the sum over none.
+constexpr int OUT_TOKENS = 2, OUT_PARTS = 8;
+
+__global__ void __launch_bounds__(256) k_few_out(const Few f, uint32_t ctas)
+{
+    // k_few_prep had completed long before phase 2 let this kernel start
+    const int n_act = __ldcg(f.n_act);
+    const int t0 = blockIdx.y * OUT_TOKENS, blk = threadIdx.x >> 7, row = threadIdx.x & 127;
+    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const Range r = few_range<2>(f, n_act ? n_act : 1, ctas);
+    const Parts p(f, r, blockIdx.x * r.per);
+    const int64_t at = (int64_t)blk * f.T * 128 + (int64_t)t0 * 128 + row;
+    wait_previous();
+    if (n >= f.N || (n_act && p.c0 == p.c1)) return;
+    float v[OUT_TOKENS];
+#pragma unroll
+    for (int i = 0; i < OUT_TOKENS; ++i) v[i] = 0.0f;
+    if (n_act) {
+#pragma unroll 1
+        for (uint32_t c = p.c0; c <= p.c1; c += OUT_PARTS) {
+            float x[OUT_PARTS][OUT_TOKENS];
+#pragma unroll
+            for (int q = 0; q < OUT_PARTS; ++q) {
+                const float* src = p.at(c + q <= p.c1 ? c + q : p.c1) + at;
+#pragma unroll
+                for (int i = 0; i < OUT_TOKENS; ++i) x[q][i] = __ldcg(src + (t0 + i < f.T ? i * 128 : 0));
+            }
+#pragma unroll
+            for (int q = 0; q < OUT_PARTS; ++q)
+#pragma unroll
+                for (int i = 0; i < OUT_TOKENS; ++i) v[i] += c + q <= p.c1 ? x[q][i] : 0.0f;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < OUT_TOKENS; ++i)
+        if (t0 + i < f.T) store_out(f, t0 + i, n, v[i]);
 }
 
 // ------------------------------------------------------------ host side
@@ -654,13 +843,33 @@ template <int NB>
 int launch_few_gemms(const Few& f, const CUtensorMap& tmW13, const CUtensorMap& tmW2, const CUtensorMap& tmX,
                      const CUtensorMap& tmA, unsigned ctas, cudaStream_t st)
 {
-    constexpr uint32_t smem = dyn_smem(NB);
+    constexpr uint32_t smem = num_stages(NB) * stage_bytes(NB) + (uint32_t)sizeof(FewShared<NB>);
+    static_assert(smem <= (NB <= 16 ? 116736u - 1024u : 232448u), "shared memory of a CTA (two per SM up to 16 tokens)");
     if (!few_allow_smem<k_few_gemm<1, NB>>((int)smem) || !few_allow_smem<k_few_gemm<2, NB>>((int)smem))
         return FP8_ERR_LAUNCH;
-    k_few_gemm<1, NB><<<ctas, NUM_THREADS, smem, st>>>(tmW13, tmX, f);
-    if (cudaGetLastError() != cudaSuccess) return FP8_ERR_LAUNCH;
-    k_few_gemm<2, NB><<<ctas, NUM_THREADS, smem, st>>>(tmW2, tmA, f);
-    return cudaGetLastError() == cudaSuccess ? FP8_OK : FP8_ERR_LAUNCH;
+    // both may start while the kernel before them in the stream still runs
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, 1, 1);
+    cfg.blockDim = dim3(num_threads(NB), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, k_few_gemm<1, NB>, tmW13, tmX, tmW2, f) != cudaSuccess) return FP8_ERR_LAUNCH;
+    const int64_t A = (int64_t)f.T * f.k < f.G ? (int64_t)f.T * f.k : f.G;
+    cudaLaunchConfig_t act = cfg;
+    act.gridDim = dim3((unsigned)(A * (f.I / 128)), (unsigned)((f.T + 31) / 32), 1);
+    act.blockDim = dim3(128, 1, 1);
+    act.dynamicSmemBytes = 0;
+    if (cudaLaunchKernelEx(&act, k_few_act, f, (uint32_t)ctas) != cudaSuccess) return FP8_ERR_LAUNCH;
+    if (cudaLaunchKernelEx(&cfg, k_few_gemm<2, NB>, tmW2, tmA, tmW2, f) != cudaSuccess) return FP8_ERR_LAUNCH;
+    cfg.gridDim = dim3((unsigned)((f.N + 255) / 256), (unsigned)((f.T + OUT_TOKENS - 1) / OUT_TOKENS), 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, k_few_out, f, (uint32_t)ctas) == cudaSuccess ? FP8_OK : FP8_ERR_LAUNCH;
 }
 
 }  // namespace

@@ -432,9 +432,9 @@ int fp8_swiglu_bwd(const uint8_t* qh, int64_t ldqh, const float* sh, const void*
  *           bytes, 256-byte aligned, contents on entry ignored; calls that may
  *           overlap (other streams, captured graphs that run at once) need one each
  * The sums are taken in a fixed order: equal inputs give equal bits.
- * Sizes: 0 <= T <= FP8_MOE_FEW_MAX_TOKENS (0 launches nothing), 1 <= k <= 1024,
+ * Sizes: 0 <= T <= FP8_MOE_FEW_MAX_TOKENS (0 launches nothing), 1 <= k <= 128,
  * 1 <= G <= 1024; K, I, N > 0 and multiples of 128; G*2I, G*N <= 2^31 - 1;
- * ldx >= K, ldo >= N.  x, W13, W2 and out 16-byte aligned.  Three kernel launches.
+ * ldx >= K, ldo >= N.  x, W13, W2 and out 16-byte aligned.  Five kernel launches.
  */
 #define FP8_MOE_FEW_MAX_TOKENS 128
 int64_t fp8_moe_mlp_few_workspace_bytes(int64_t T, int k, int G, int64_t K, int64_t I, int64_t N);

@@ -81,7 +81,7 @@ def test_moe_mlp_few_validation(lib):
     assert need > 0
     for kw in (dict(dt=2), dict(od=2), dict(mode=2)):
         assert call(**kw) == fg.FP8_ERR_DTYPE
-    for kw in (dict(T=-1), dict(T=fg.MOE_FEW_MAX_TOKENS + 1), dict(k=0), dict(k=1025), dict(G=0), dict(G=1025),
+    for kw in (dict(T=-1), dict(T=fg.MOE_FEW_MAX_TOKENS + 1), dict(k=0), dict(k=129), dict(G=0), dict(G=1025),
                dict(K=200), dict(K=0), dict(I=64), dict(I=0), dict(N=100), dict(N=0), dict(ldx=128),
                dict(ldo=256), dict(wsb=need - 1), dict(G=1024, I=1 << 21), dict(G=1024, N=1 << 22, ldo=1 << 22)):
         assert call(**kw) == fg.FP8_ERR_SHAPE, kw
