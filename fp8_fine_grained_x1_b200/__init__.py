@@ -336,24 +336,34 @@ def fp8_moe_combine(D, token_row, weights, out, stream=None) -> None:
 # before the pointers reach the library, and run on the device of their first
 # input whichever device is current.
 
-def _need(t, name, dtype, shape, device, contiguous=False):
-    """`t` is a device tensor of this dtype and shape with unit stride along its last axis."""
-    if t.dtype != dtype:
+def _rows(t, name, dtype, shape, dev):
+    """Row stride of `t`, which must be a tensor of this dtype and shape on CUDA device `dev` with
+    unit stride along its last axis (a short path for what is right, and one that says what is not:
+    these calls' GPU time can be a few microseconds)."""
+    if t.dtype is dtype and t.get_device() == dev >= 0 and t.shape == shape:
+        if t.is_contiguous():
+            return shape[-1]
+        if t.dim() == 2 and t.stride(1) == 1:
+            return t.stride(0)
+    _refuse(t, name, dtype, shape, dev)
+
+
+def _flat(t, name, dtype, shape, dev):
+    """Address of `t`, which must be contiguous, of this dtype and shape, on CUDA device `dev`."""
+    if t.dtype is dtype and t.get_device() == dev >= 0 and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, dev)
+
+
+def _refuse(t, name, dtype, shape, dev):
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be on the CUDA device of the first input ({device}), got {t.device}")
+    if dev < 0 or t.get_device() != dev:
+        raise ValueError(f"{name} must be on the CUDA device of the first input, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if contiguous:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    elif t.stride(-1) != 1 and shape[-1] > 1 and t.numel():
-        raise ValueError(f"{name} must have unit stride along its last axis")
-
-
-def _row(t, cols):
-    """Row stride of a 2-D tensor (its width when it has fewer than two rows)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), cols)
+    raise ValueError(f"{name}: a matrix must have unit stride along its rows, other tensors must be "
+                     f"contiguous; got strides {tuple(t.stride())}")
 
 
 def _pair(a, b, what):
@@ -362,18 +372,20 @@ def _pair(a, b, what):
     return a is not None
 
 
-def _call_on(device, stream, fn, where, *args):
-    """fn(*args, stream) with `device` current and its current stream unless one is given."""
+def _call_on(dev, stream, fn, where, *args):
+    """fn(*args, stream) with device `dev` current, on its current stream unless one is given."""
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"{where}: stream of {stream.device}, tensors on {device}")
-    if torch.cuda.current_device() == device.index:
-        code = fn(*args, stream.cuda_stream)
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device_index != dev:
+        raise ValueError(f"{where}: stream of cuda:{stream.device_index}, tensors on cuda:{dev}")
     else:
-        with torch.cuda.device(device):
-            code = fn(*args, stream.cuda_stream)
+        raw = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        code = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, raw)
     if code != FP8_OK:
         raise Fp8Error(code, where)
 
@@ -388,19 +400,17 @@ def fp8_swiglu_quant(h, qa, sa, qh=None, sh=None, n_rows=None, scale_mode: int =
     u8, f32 = torch.uint8, torch.float32
     M, C = h.shape
     I = C // 2
-    d = h.device
-    _need(h, "h", h.dtype, (M, 2 * I), d)
-    _need(qa, "qa", u8, (M, I), d)
-    _need(sa, "sa", f32, (I // 128, M), d, True)
-    keep = _pair(qh, sh, "qh and sh")
-    if keep:
-        _need(qh, "qh", u8, (M, C), d)
-        _need(sh, "sh", f32, (C // 128, M), d, True)
-    if n_rows is not None:
-        _need(n_rows, "n_rows", torch.int32, (1,), d)
+    d = h.get_device()
+    ldh = _rows(h, "h", h.dtype, (M, 2 * I), d)
+    ldqa = _rows(qa, "qa", u8, (M, I), d)
+    psa = _flat(sa, "sa", f32, (I // 128, M), d)
+    pqh, ldqh, psh = None, 0, None
+    if _pair(qh, sh, "qh and sh"):
+        ldqh, pqh = _rows(qh, "qh", u8, (M, C), d), qh.data_ptr()
+        psh = _flat(sh, "sh", f32, (C // 128, M), d)
     _call_on(d, stream, load_library().fp8_swiglu_quant, "fp8_swiglu_quant",
-             _ptr(h), _in_dtype(h), M, I, _row(h, C), _ptr(qa), _row(qa, I), _ptr(sa),
-             _ptr(qh), _row(qh, C) if keep else 0, _ptr(sh), _ptr(n_rows), scale_mode)
+             h.data_ptr(), _in_dtype(h), M, I, ldh, qa.data_ptr(), ldqa, psa, pqh, ldqh, psh,
+             None if n_rows is None else _flat(n_rows, "n_rows", torch.int32, (1,), d), scale_mode)
 
 
 def fp8_swiglu_bwd(qh, sh, da, dh=None, qdh=None, sdh=None, qdhT=None, sdhT=None, qaT=None,
@@ -412,32 +422,27 @@ def fp8_swiglu_bwd(qh, sh, da, dh=None, qdh=None, sdh=None, qdhT=None, sdhT=None
     u8, f32 = torch.uint8, torch.float32
     M, C = qh.shape
     I = C // 2
-    d = qh.device
-    _need(qh, "qh", u8, (M, 2 * I), d)
-    _need(sh, "sh", f32, (C // 128, M), d, True)
-    _need(da, "da", da.dtype, (M, I), d)
-    if dh is not None:
-        _need(dh, "dh", torch.bfloat16, (M, C), d)
-    rows = _pair(qdh, sdh, "qdh and sdh")
-    if rows:
-        _need(qdh, "qdh", u8, (M, C), d)
-        _need(sdh, "sdh", f32, (C // 128, M), d, True)
-    cols = _pair(qdhT, sdhT, "qdhT and sdhT")
-    if cols:
-        _need(qdhT, "qdhT", u8, (C, M), d)
-        _need(sdhT, "sdhT", f32, (M // 128, C), d, True)
-    act = _pair(qaT, saT, "qaT and saT")
-    if act:
-        _need(qaT, "qaT", u8, (I, M), d)
-        _need(saT, "saT", f32, (M // 128, I), d, True)
-    if n_rows is not None:
-        _need(n_rows, "n_rows", torch.int32, (1,), d)
+    d = qh.get_device()
+    ldqh = _rows(qh, "qh", u8, (M, 2 * I), d)
+    psh = _flat(sh, "sh", f32, (C // 128, M), d)
+    ldda = _rows(da, "da", da.dtype, (M, I), d)
+    pdh, lddh = (None, 0) if dh is None else (dh.data_ptr(), _rows(dh, "dh", torch.bfloat16, (M, C), d))
+    pqdh, ldqdh, psdh = None, 0, None
+    if _pair(qdh, sdh, "qdh and sdh"):
+        ldqdh, pqdh = _rows(qdh, "qdh", u8, (M, C), d), qdh.data_ptr()
+        psdh = _flat(sdh, "sdh", f32, (C // 128, M), d)
+    pqdhT, ldqdhT, psdhT = None, 0, None
+    if _pair(qdhT, sdhT, "qdhT and sdhT"):
+        ldqdhT, pqdhT = _rows(qdhT, "qdhT", u8, (C, M), d), qdhT.data_ptr()
+        psdhT = _flat(sdhT, "sdhT", f32, (M // 128, C), d)
+    pqaT, ldqaT, psaT = None, 0, None
+    if _pair(qaT, saT, "qaT and saT"):
+        ldqaT, pqaT = _rows(qaT, "qaT", u8, (I, M), d), qaT.data_ptr()
+        psaT = _flat(saT, "saT", f32, (M // 128, I), d)
     _call_on(d, stream, load_library().fp8_swiglu_bwd, "fp8_swiglu_bwd",
-             _ptr(qh), _row(qh, C), _ptr(sh), _ptr(da), _in_dtype(da), _row(da, I), M, I,
-             _ptr(dh), _row(dh, C) if dh is not None else 0,
-             _ptr(qdh), _row(qdh, C) if rows else 0, _ptr(sdh),
-             _ptr(qdhT), _row(qdhT, M) if cols else 0, _ptr(sdhT),
-             _ptr(qaT), _row(qaT, M) if act else 0, _ptr(saT), _ptr(n_rows), scale_mode)
+             qh.data_ptr(), ldqh, psh, da.data_ptr(), _in_dtype(da), ldda, M, I, pdh, lddh,
+             pqdh, ldqdh, psdh, pqdhT, ldqdhT, psdhT, pqaT, ldqaT, psaT,
+             None if n_rows is None else _flat(n_rows, "n_rows", torch.int32, (1,), d), scale_mode)
 
 
 def fp8_moe_mlp_few_workspace_bytes(T: int, k: int, G: int, K: int, I: int, N: int) -> int:
@@ -457,20 +462,15 @@ def fp8_moe_mlp_few(x, topk, weights, W13, s13, W2, s2, out, workspace,
     G, C, _ = W13.shape
     N = W2.shape[1]
     I = C // 2
-    d = x.device
-    _need(x, "x", x.dtype, (T, K), d)
-    _need(topk, "topk", torch.int32, (T, k), d, True)
-    _need(weights, "weights", f32, (T, k), d, True)
-    _need(W13, "W13", u8, (G, 2 * I, K), d, True)
-    _need(s13, "s13", f32, (G, C // 128, K // 128), d, True)
-    _need(W2, "W2", u8, (G, N, I), d, True)
-    _need(s2, "s2", f32, (G, N // 128, I // 128), d, True)
-    _need(out, "out", out.dtype, (T, N), d)
-    _need(workspace, "workspace", u8, workspace.shape, d, True)
+    d = x.get_device()
+    ldx = _rows(x, "x", x.dtype, (T, K), d)
+    ldo = _rows(out, "out", out.dtype, (T, N), d)
     _call_on(d, stream, load_library().fp8_moe_mlp_few, "fp8_moe_mlp_few",
-             _ptr(x), _in_dtype(x), T, K, _row(x, K), _ptr(topk), _ptr(weights), k, G, _ptr(W13),
-             _ptr(s13), _ptr(W2), _ptr(s2), I, N, _ptr(out), _out_dtype(out), _row(out, N),
-             _ptr(workspace), workspace.numel(), scale_mode)
+             x.data_ptr(), _in_dtype(x), T, K, ldx, _flat(topk, "topk", torch.int32, (T, k), d),
+             _flat(weights, "weights", f32, (T, k), d), k, G, _flat(W13, "W13", u8, (G, 2 * I, K), d),
+             _flat(s13, "s13", f32, (G, C // 128, K // 128), d), _flat(W2, "W2", u8, (G, N, I), d),
+             _flat(s2, "s2", f32, (G, N // 128, I // 128), d), I, N, out.data_ptr(), _out_dtype(out),
+             ldo, _flat(workspace, "workspace", u8, (workspace.numel(),), d), workspace.numel(), scale_mode)
 
 
 def fp8_get_status(stream=None) -> int:

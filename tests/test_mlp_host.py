@@ -107,32 +107,42 @@ def test_python_calls_refuse_host_tensors_and_wrong_layouts(lib):
         fg.moe_mlp_few(h, torch.zeros((128, 2), dtype=torch.int32), torch.zeros((128, 2)),
                        torch.zeros((4, 256, 512), dtype=u8), torch.zeros((4, 2, 4)),
                        torch.zeros((4, 512, 128), dtype=u8), torch.zeros((4, 4, 1)))
-    d = torch.device("cuda", 0)
 
-    class Fake:      # what _need looks at, without a device
-        def __init__(self, shape, dtype, stride=None, cont=True):
-            self.shape, self.dtype, self.device, self.is_cuda = torch.Size(shape), dtype, d, True
-            self._st, self._c = stride or (shape[-1], 1), cont
+    class Fake:      # what the checks look at, without a device
+        def __init__(self, shape, dtype, stride=None, cont=True, dev=0):
+            self.shape, self.dtype, self.device = torch.Size(shape), dtype, f"cuda:{dev}"
+            self._st, self._c, self._d = stride or (shape[-1], 1), cont, dev
 
-        def stride(self, i):
-            return self._st[i]
+        def get_device(self):
+            return self._d
+
+        def dim(self):
+            return len(self.shape)
+
+        def stride(self, i=None):
+            return self._st if i is None else self._st[i]
 
         def is_contiguous(self):
             return self._c
 
-        def numel(self):
-            return self.shape.numel()
-    fg._need(Fake((4, 8), u8), "q", u8, (4, 8), d)
-    with pytest.raises(TypeError):
-        fg._need(Fake((4, 8), f32), "q", u8, (4, 8), d)
-    with pytest.raises(ValueError, match="shape"):
-        fg._need(Fake((4, 9), u8), "q", u8, (4, 8), d)
+        def data_ptr(self):
+            return 64
+    assert fg._rows(Fake((4, 8), u8), "q", u8, (4, 8), 0) == 8
+    assert fg._rows(Fake((4, 8), u8, (24, 1), False), "q", u8, (4, 8), 0) == 24
+    assert fg._flat(Fake((4, 8), u8), "q", u8, (4, 8), 0) == 64
+    for check in (fg._rows, fg._flat):
+        with pytest.raises(TypeError):
+            check(Fake((4, 8), f32), "q", u8, (4, 8), 0)
+        with pytest.raises(ValueError, match="shape"):
+            check(Fake((4, 9), u8), "q", u8, (4, 8), 0)
+        with pytest.raises(ValueError, match="stride"):
+            check(Fake((4, 8), u8, (1, 4), False), "q", u8, (4, 8), 0)
+        with pytest.raises(ValueError, match="device"):
+            check(Fake((4, 8), u8), "q", u8, (4, 8), 1)
+        with pytest.raises(ValueError, match="device"):
+            check(Fake((4, 8), u8, dev=-1), "q", u8, (4, 8), -1)
     with pytest.raises(ValueError, match="stride"):
-        fg._need(Fake((4, 8), u8, (1, 4)), "q", u8, (4, 8), d)
-    with pytest.raises(ValueError, match="contiguous"):
-        fg._need(Fake((4, 8), u8, cont=False), "q", u8, (4, 8), d, True)
-    with pytest.raises(ValueError, match="device"):
-        fg._need(Fake((4, 8), u8), "q", u8, (4, 8), torch.device("cuda", 1))
+        fg._flat(Fake((4, 8), u8, (24, 1), False), "q", u8, (4, 8), 0)
     with pytest.raises(ValueError, match="together"):
         fg._pair(h, None, "qh and sh")
 
