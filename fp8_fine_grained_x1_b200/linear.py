@@ -18,6 +18,13 @@ from it and joined back before the GEMM:
                contiguous, 128-padded FP8 rows-->; W[G,N,K] --128x128-->;
                grouped GEMM (or, gather=True, quantized once and gathered by
                the GEMM)
+  GatedMlpStep X[M,K] . W13[2I,K]^T -> SwiGLU -> . W2[N,I]^T, forward and
+               backward: what backward needs is kept in FP8 (X's codes and the
+               SwiGLU's 8-bit checkpoint), and the SwiGLU writes and reads the
+               operands of the GEMMs around it
+  MoeMlpStep   the MoE layer's MLP with weights already in FP8: up to
+               MOE_FEW_MAX_TOKENS tokens in one call (fp8_moe_mlp_few), more
+               through the dispatch and two grouped GEMMs
 
 ("5 Ways You can get More Deepseek While Spending Less", Figure 6: Fprop,
 Dgrad and Wgrad all run in FP8; why-be.co.kr / cameseeing.com posts and
@@ -35,12 +42,13 @@ from __future__ import annotations
 
 import torch
 
-from . import (B_KMAJOR, B_MNMAJOR, SCALE_FP32, SCALE_POW2, fp8_blockscaled_gemm,
+from . import (B_KMAJOR, B_MNMAJOR, MOE_FEW_MAX_TOKENS, SCALE_FP32, SCALE_POW2, fp8_blockscaled_gemm,
                fp8_blockscaled_gemm_pow2, fp8_grouped_gemm, fp8_grouped_gemm_gather,
                fp8_grouped_gemm_pow2,
-               fp8_moe_combine, fp8_moe_dispatch_workspace_bytes, fp8_moe_quant_dispatch,
+               fp8_moe_combine, fp8_moe_dispatch_workspace_bytes, fp8_moe_mlp_few,
+               fp8_moe_mlp_few_workspace_bytes, fp8_moe_quant_dispatch,
                fp8_moe_route, fp8_quant_act_128x1, fp8_quant_act_1x128, fp8_quant_w_128x128,
-               fp8_requant_1x128_to_128x1, moe_capacity)
+               fp8_requant_1x128_to_128x1, fp8_swiglu_bwd, fp8_swiglu_quant, moe_capacity)
 
 
 def _empty(shape, dtype, device):
@@ -298,3 +306,142 @@ class MoeStep:
         self.quantize(stream)
         self.gemm(stream)
         return self.y
+
+
+class GatedMlpStep:
+    """Gated MLP, forward and backward: H = X . W13^T (W13 [2I, K]: gate rows,
+    then up rows), A = silu(gate) * up, Y = A . W2^T (W2 [N, I]).
+
+    Calling the step runs the forward pass and returns Y.  `backward(dy)` (dy
+    [M, N] BF16 or FP32, M a multiple of 128) returns dX (out_dtype), dW13 and
+    dW2 (FP32).  Between the two the step keeps, in FP8, X's 1x128 codes and H's
+    (`qx`, `qh`: 3 bytes per token and channel of K and of I where BF16 X, H and A
+    would take 2 K + 6 I); H in BF16 is scratch, and A is recomputed.  Weights are
+    quantized in the forward pass and reused by backward."""
+    kernel_calls = 6             # x, w13, w2 quantizers, two GEMMs, the SwiGLU
+    kernel_calls_backward = 8    # dy twice, cached x, the SwiGLU, four GEMMs
+
+    def __init__(self, x, w13, w2, out_dtype=torch.bfloat16, scale_mode=SCALE_FP32):
+        M, K = x.shape
+        C, K2 = w13.shape
+        N, I = w2.shape
+        if K != K2 or C != 2 * I:
+            raise ValueError(f"x {tuple(x.shape)}, w13 {tuple(w13.shape)} and w2 {tuple(w2.shape)} do not fit: "
+                             "w13 is [2I, K] and w2 [N, I]")
+        d = x.device
+        u8, f32 = torch.uint8, torch.float32
+        self.x, self.w13, self.w2, self.mode, self.out_dtype = x, w13, w2, scale_mode, out_dtype
+        self.qx, self.sx = _empty((M, K), u8, d), _empty((K // 128, M), f32, d)
+        self.qw13, self.sw13 = _empty((C, K), u8, d), _empty((C // 128, K // 128), f32, d)
+        self.qw2, self.sw2 = _empty((N, I), u8, d), _empty((N // 128, I // 128), f32, d)
+        self.h = _empty((M, C), torch.bfloat16, d)
+        self.qh, self.sh = _empty((M, C), u8, d), _empty((C // 128, M), f32, d)
+        self.qa, self.sa = _empty((M, I), u8, d), _empty((I // 128, M), f32, d)
+        self.y = _empty((M, N), out_dtype, d)
+        self.flops = 2 * M * (C * K + N * I)
+        self.inputs, self.output = [x, w13, w2], self.y
+        self._fork = _Fork(d)
+        self._grad = None
+
+    def __call__(self, stream=None):
+        cur, side = self._fork.begin(stream)
+        fp8_quant_w_128x128(self.w13, self.qw13, self.sw13, self.mode, side)
+        fp8_quant_w_128x128(self.w2, self.qw2, self.sw2, self.mode, side)
+        fp8_quant_act_1x128(self.x, self.qx, self.sx, self.mode, cur)
+        self._fork.end(cur)
+        fp8_blockscaled_gemm(self.qx, self.sx, self.qw13, self.sw13, self.h, B_KMAJOR, 128, cur)
+        fp8_swiglu_quant(self.h, self.qa, self.sa, self.qh, self.sh, None, self.mode, cur)
+        fp8_blockscaled_gemm(self.qa, self.sa, self.qw2, self.sw2, self.y, B_KMAJOR, 128, cur)
+        return self.y
+
+    def _gradient_buffers(self):
+        if self._grad is None:
+            M, K = self.x.shape
+            N, I = self.w2.shape
+            d, u8, f32 = self.x.device, torch.uint8, torch.float32
+            if M % 128:
+                raise ValueError(f"backward needs whole groups of 128 tokens, got {M}")
+            self._grad = dict(
+                qdy=_empty((M, N), u8, d), sdy=_empty((N // 128, M), f32, d),
+                qdyT=_empty((N, M), u8, d), sdyT=_empty((M // 128, N), f32, d),
+                da=_empty((M, I), torch.bfloat16, d),
+                qdh=_empty((M, 2 * I), u8, d), sdh=_empty((2 * I // 128, M), f32, d),
+                qdhT=_empty((2 * I, M), u8, d), sdhT=_empty((M // 128, 2 * I), f32, d),
+                qaT=_empty((I, M), u8, d), saT=_empty((M // 128, I), f32, d),
+                qxT=_empty((K, M), u8, d), sxT=_empty((M // 128, K), f32, d),
+                dx=_empty((M, K), self.out_dtype, d), dw13=_empty((2 * I, K), f32, d), dw2=_empty((N, I), f32, d))
+        return self._grad
+
+    def backward(self, dy, stream=None):
+        g = self._gradient_buffers()
+        cur, side = self._fork.begin(stream)
+        # dy along tokens and x's cached codes regrouped, for the two Wgrads
+        fp8_quant_act_128x1(dy, g["qdyT"], g["sdyT"], self.mode, side)
+        fp8_requant_1x128_to_128x1(self.qx, self.sx, g["qxT"], g["sxT"], self.mode, side)
+        fp8_quant_act_1x128(dy, g["qdy"], g["sdy"], self.mode, cur)
+        fp8_blockscaled_gemm(g["qdy"], g["sdy"], self.qw2, self.sw2, g["da"], B_MNMAJOR, 128, cur)
+        fp8_swiglu_bwd(self.qh, self.sh, g["da"], qdh=g["qdh"], sdh=g["sdh"], qdhT=g["qdhT"], sdhT=g["sdhT"],
+                       qaT=g["qaT"], saT=g["saT"], scale_mode=self.mode, stream=cur)
+        fp8_blockscaled_gemm(g["qdh"], g["sdh"], self.qw13, self.sw13, g["dx"], B_MNMAJOR, 128, cur)
+        self._fork.end(cur)
+        fp8_blockscaled_gemm(g["qdhT"], g["sdhT"], g["qxT"], g["sxT"], g["dw13"], B_KMAJOR, 1, cur)
+        fp8_blockscaled_gemm(g["qdyT"], g["sdyT"], g["qaT"], g["saT"], g["dw2"], B_KMAJOR, 1, cur)
+        return g["dx"], g["dw13"], g["dw2"]
+
+
+class MoeMlpStep:
+    """The MLP of an MoE layer in inference: out[t] = sum_j weights[t, j] *
+    W2_e . (silu(gate) * up) with [gate | up] = W13_e . x[t], e = topk[t, j], on
+    weights quantized beforehand (qw13 [G, 2I, K], sw13; qw2 [G, N, I], sw2).
+
+    Up to MOE_FEW_MAX_TOKENS tokens take one call that reads each active
+    expert's weights once (fp8_moe_mlp_few).  More tokens are quantized and
+    dispatched to 128-padded groups, and the SwiGLU between the two grouped GEMMs
+    quantizes the rows in use for the second; H is BF16 there and FP32 in the few-token form.  `few`
+    overrides the choice."""
+
+    def __init__(self, x, topk, weights, qw13, sw13, qw2, sw2, out_dtype=torch.bfloat16, scale_mode=SCALE_FP32,
+                 few=None):
+        T, K = x.shape
+        k = topk.shape[1]
+        G, C, _ = qw13.shape
+        N, I = qw2.shape[1:]
+        d, u8, f32 = x.device, torch.uint8, torch.float32
+        self.few = T <= MOE_FEW_MAX_TOKENS if few is None else few
+        if self.few and T > MOE_FEW_MAX_TOKENS:
+            raise ValueError(f"the few-token form takes {MOE_FEW_MAX_TOKENS} tokens, got {T}")
+        if not self.few and out_dtype != torch.bfloat16:
+            raise ValueError("the combine of the dispatched form writes BF16")
+        self.x, self.topk, self.weights, self.mode, self.G = x, topk, weights, scale_mode, G
+        self.qw13, self.sw13, self.qw2, self.sw2 = qw13, sw13, qw2, sw2
+        self.out = _empty((T, N), out_dtype, d)
+        self.inputs, self.output = [x, topk, weights], self.out
+        # the few-token form: preparation, two GEMMs, SwiGLU, output sums; the other: routing (3), fused
+        # quantizer, padding rows, two grouped GEMMs, SwiGLU, combine (+1 memset)
+        self.kernel_calls = 5 if self.few else 9
+        if self.few:
+            n = fp8_moe_mlp_few_workspace_bytes(T, k, G, K, I, N)
+            self.ws = _empty((max(n, 1),), u8, d)
+            return
+        M = moe_capacity(T, k, G)
+        self.qr, self.sr = _empty((M, K), u8, d), _empty((K // 128, M), f32, d)
+        self.offsets = _empty((G + 1,), torch.int32, d)
+        self.token_row = _empty((T, k), torch.int32, d)
+        self.row_token = _empty((M,), torch.int32, d)
+        self.ws = _empty((max(1, fp8_moe_dispatch_workspace_bytes(T, k, G) // 4),), torch.int32, d)
+        self.h = _empty((M, C), torch.bfloat16, d)
+        self.qa, self.sa = _empty((M, I), u8, d), _empty((I // 128, M), f32, d)
+        self.y = _empty((M, N), torch.bfloat16, d)
+
+    def __call__(self, stream=None):
+        if self.few:
+            fp8_moe_mlp_few(self.x, self.topk, self.weights, self.qw13, self.sw13, self.qw2, self.sw2, self.out,
+                            self.ws, self.mode, stream)
+            return self.out
+        fp8_moe_quant_dispatch(self.x, self.topk, self.G, self.qr, self.sr, self.offsets, self.token_row,
+                               self.row_token, self.ws, self.mode, stream)
+        fp8_grouped_gemm(self.qr, self.sr, self.qw13, self.sw13, self.offsets, self.h, stream)
+        fp8_swiglu_quant(self.h, self.qa, self.sa, n_rows=self.offsets[self.G:], scale_mode=self.mode, stream=stream)
+        fp8_grouped_gemm(self.qa, self.sa, self.qw2, self.sw2, self.offsets, self.y, stream)
+        fp8_moe_combine(self.y, self.token_row, self.weights, self.out, stream)
+        return self.out
