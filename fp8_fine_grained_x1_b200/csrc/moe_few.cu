@@ -7,29 +7,29 @@
 // With this few tokens the layer is bound by reading the active experts'
 // weights once from HBM ("Three Fast Methods To Study Deepseek": top-8
 // routing; gnrental.net post: the MoE part reads one expert's weights per
-// group).  So the weights are the M operand (128 rows per MMA) and the tokens
-// its N columns, and no rows are gathered or padded to 128: every column of an
-// expert's products is a token, whether it was routed to that expert or not.
-// The columns the tensor cores compute in vain cost nothing next to the
-// weight stream (128 columns: 0.8 us per 32 KB of weights against 0.75 for
-// reading them), the B operand is the same token matrix for every expert, and
-// the combine happens in the accumulator: column t of expert e's second
-// product is promoted with its activation's scale times t's gate weight for e
-// (0, and zero codes, where e was not picked).
+// group).  So no rows are gathered or padded to 128 per expert: the products
+// of an expert's weights are made with all tokens, whether they were routed to
+// it or not.  What the tensor cores compute in vain costs nothing next to the
+// weight stream, the token operand is the same for every expert, and the
+// combine happens in the accumulator: token t's part of expert e's second
+// product is promoted with its activation's scale times t's gate weight for e,
+// and left out where e was not picked.  Up to 32 tokens are the N columns of
+// the MMAs and the weights their M rows, more tokens are the M rows (see
+// MAX_COLUMN_TOKENS).
 //
 // Kernels, in stream order (each starts while the one before drains):
 //   k_few_prep      codes and scales of x, the gate-weight table [expert][token],
 //                   the list of active experts
 //   k_few_gemm<1>   persistent; tile = 128 gate + 128 up rows of an expert over K;
 //                   leaves the sums, or its parts of them, in scratch
-//   k_few_act       adds the parts; SwiGLU and 1x128 quantization
+//   k_few_act, k_few_act_rows   adds the parts; SwiGLU and 1x128 quantization
 //   k_few_gemm<2>   persistent; tile = 256 output columns over all (expert, I);
 //                   whole tiles are rounded and stored, parts left in scratch
 //   k_few_out       adds the parts, rounds
 //
 // Both GEMM kernels lay their tiles' K-blocks end to end and give every CTA an
-// equal contiguous range of them (stream-K), so all SMs stream weights for the
-// same time whatever the tile count.  Parts of a tile are added in CTA order,
+// equal contiguous range of them (stream-K), so all SMs stream weights whatever
+// the tile count.  Parts of a tile are added in CTA order,
 // so results do not depend on timing.  The adding is done by kernels of its own:
 // inside the GEMMs, by the CTA that finished a tile last, it held up that CTA's
 // weight stream (128 tokens: 15 us per tile of phase 1, 35 us per tile of phase
@@ -59,10 +59,10 @@ constexpr uint32_t W_BYTES = 2 * WBLK_BYTES;    // two row blocks per stage
 constexpr int NUM_PROMO_WARPS = 8;              // warps 0-3: block 0, 4-7: block 1
 constexpr int PROMO_THREADS = 32 * NUM_PROMO_WARPS;
 constexpr int WARP_TMA = 8, WARP_MMA = 9;
-// 128 token columns need more promotion registers than an even split gives: the kernel then
-// launches a third whole warpgroup (TMA, MMA, 2 idle warps), which hands its registers over.
+// The row form's 128 accumulators need more promotion registers than an even split gives: the kernel
+// then launches a third whole warpgroup (TMA, MMA, 2 idle warps), which hands its registers over.
 // (Spilled, the accumulators went through L2 -- shared memory leaves no L1 -- at 3 us per unit.)
-__host__ __device__ constexpr int num_threads(int nb) { return nb > 64 ? 384 : PROMO_THREADS + 64; }
+__host__ __device__ constexpr int num_threads(int nb) { return nb == 128 ? 384 : PROMO_THREADS + 64; }
 constexpr uint32_t LAUNCH_REGS = 168, CTRL_REGS = 72, PROMO_REGS = 216;
 static_assert(128 * CTRL_REGS + 256 * PROMO_REGS <= 384 * LAUNCH_REGS, "register split exceeds the launch allocation");
 constexpr int SLOTS = 8;                        // scale slots (at least MAX_STAGES + 2, see FewShared)
@@ -73,6 +73,13 @@ constexpr uint32_t MIN_UNITS = 2;
 // then load while phase 1 drains); more tokens get one CTA with a deeper ring.
 __host__ __device__ constexpr uint32_t ring_budget(int nb) { return (nb <= 16 ? 104 : 216) * 1024; }
 __host__ __device__ constexpr uint32_t stage_bytes(int nb) { return W_BYTES + (uint32_t)nb * BK; }
+// Up to MAX_COLUMN_TOKENS tokens are the columns of the products (NB of them: 16 or 32), more are the 128
+// rows.  A thread of the column form needs every token's scale, from shared memory, for each unit, and
+// the MMAs read the weights 128 rows at a time for few columns; one of the row form needs one scale, but
+// its stage always holds 128 token rows (4 stages instead of 6).  Of 16 experts of 7168 x 2048, columns
+// took 144 us for 17 tokens and 167 for 64 (accumulators of 64), rows 154 and 151 to 156.
+constexpr int MAX_COLUMN_TOKENS = 32;
+__host__ __device__ constexpr bool token_rows(int nb) { return nb == 128; }
 __host__ __device__ constexpr int num_stages(int nb)
 {
     const int n = (int)(ring_budget(nb) / stage_bytes(nb));
@@ -101,8 +108,8 @@ struct Few {
     float* xs;
     uint8_t* aq;            // [A * Tp][I] codes, as [A][I/128][Tp] scales * gate weight
     float* as;
-    float* part;            // [2 * CTAs][2][T][128] parts of tiles that several CTAs share
-    float* whole;           // [A * I/128][2][T][128] phase 1's other tiles
+    float* part;            // [2 * CTAs][2][T * 128] parts of tiles that several CTAs share
+    float* whole;           // [A * I/128][2][T * 128] phase 1's other tiles
 };
 
 int few_tp(int64_t T) { return (int)((T + 15) / 16 * 16); }
@@ -480,7 +487,7 @@ __device__ void few_mma(const Few& f, const Range& r, uint8_t* smem, FewShared<N
 {
     constexpr int NS = num_stages(NB);
     const uint32_t base = smem_u32(smem);
-    const uint32_t idesc = idesc_e4m3_f32(128, (uint32_t)f.Tp, 0);
+    const uint32_t idesc = token_rows(NB) ? idesc_e4m3_f32(128, 256, 0) : idesc_e4m3_f32(128, (uint32_t)f.Tp, 0);
     const uint32_t units = r.u1 - r.u0;
 #pragma unroll 1
     for (uint32_t it = 0; it < units; ++it) {
@@ -495,8 +502,13 @@ __device__ void few_mma(const Few& f, const Range& r, uint8_t* smem, FewShared<N
 #pragma unroll
         for (int k = 0; k < BK / 32; ++k) {
             const uint64_t xd = smem_desc_sw128(wa + W_BYTES + k * 32, 16, 1024);
-            mma_f8f6f4(d, smem_desc_sw128(wa + k * 32, 16, 1024), xd, idesc, k > 0);
-            mma_f8f6f4(d + NB, smem_desc_sw128(wa + WBLK_BYTES + k * 32, 16, 1024), xd, idesc, k > 0);
+            const uint64_t wd = smem_desc_sw128(wa + k * 32, 16, 1024);
+            if (token_rows(NB)) {       // the two row blocks are 256 adjacent rows
+                mma_f8f6f4(d, xd, wd, idesc, k > 0);
+            } else {
+                mma_f8f6f4(d, wd, xd, idesc, k > 0);
+                mma_f8f6f4(d + NB, smem_desc_sw128(wa + WBLK_BYTES + k * 32, 16, 1024), xd, idesc, k > 0);
+            }
         }
         mma_commit(&sh.empty[s]);
         mma_commit(&sh.tfull[buf]);
@@ -505,7 +517,12 @@ __device__ void few_mma(const Few& f, const Range& r, uint8_t* smem, FewShared<N
     mbar_wait_drain(&sh.drain, 0, f.timeout_ns);
 }
 
-// The parts of a tile: CTAs c0..c1 hold one each, in slots of `stride` floats [2][T][128].
+// Where channel c of token t lies in a row block's T x 128 sums: as the promotion's threads, one a
+// channel or one a token, can write them whole lines at a time.
+__device__ __forceinline__ int sum_at(const Few& f, int c) { return f.Tp > MAX_COLUMN_TOKENS ? (c >> 2) * f.T * 4 + (c & 3) : c; }
+__device__ __forceinline__ int sum_step(const Few& f) { return f.Tp > MAX_COLUMN_TOKENS ? 4 : 128; }      // to the next token
+
+// The parts of a tile: CTAs c0..c1 hold one each, in slots of `stride` floats, see sum_at.
 struct Parts {
     const float* part;
     Range r;
@@ -531,9 +548,29 @@ __device__ __forceinline__ void store_out(const Few& f, int t, int64_t n, float 
         static_cast<float*>(f.out)[t * f.ldo + n] = v;
 }
 
+// Eight adjacent outputs of a token (rows are 16-byte aligned).
+__device__ __forceinline__ void store_out8(const Few& f, int t, int64_t n, const float* v)
+{
+    if (f.out_dtype == FP8_OUT_BF16) {
+        uint32_t r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            r[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(f.out) + t * f.ldo + n) = make_uint4(r[0], r[1], r[2], r[3]);
+    } else {
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(f.out) + t * f.ldo + n);
+        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+}
+
+// The promotion with tokens as the accumulator's columns: thread = row of a block of the weights.
 template <int PHASE, int NB>
 __device__ void few_promotion(const Few& f, const Range& r, FewShared<NB>& sh)
 {
+    static_assert(NB <= 32, "a column's tokens are bits of one word");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int blk = warp >> 2, row = tid & 127;
     const uint32_t tmem = sh.tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + blk * NB;
@@ -543,19 +580,10 @@ __device__ void few_promotion(const Few& f, const Range& r, FewShared<NB>& sh)
     Walk<PHASE> k(f, sh.experts.id, r);
     for (; k.u < r.u1; ++seg) {
         const uint32_t tile = k.tile, tile_u0 = k.u - k.kb;
-        // phase 1: the gate weights for the tile's expert (lane l: tokens l, l + 32, ...), and which
-        // tokens were routed to it (weight not 0): only their columns matter
-        constexpr int NW = (NB + 31) / 32;
-        float gw[NW];
-        uint32_t routed[NW];
-        if (PHASE == 1) {
-#pragma unroll
-            for (int i = 0; i < NW; ++i) {
-                const int t = 32 * i + lane;
-                gw[i] = t < f.T ? __ldcg(f.gate + (int64_t)k.e * f.Tp + t) : 0.0f;
-                routed[i] = __ballot_sync(0xffffffffu, gw[i] != 0.0f);
-            }
-        }
+        // phase 1: which tokens were routed to the tile's expert (gate weight not 0)
+        uint32_t routed = 0;
+        if (PHASE == 1)
+            routed = __ballot_sync(0xffffffffu, lane < f.T && __ldcg(f.gate + (int64_t)k.e * f.Tp + lane) != 0.0f);
         const uint32_t end = r.u1 < tile_u0 + r.per ? r.u1 : tile_u0 + r.per;
         float acc[NB];
 #pragma unroll
@@ -569,26 +597,27 @@ __device__ void few_promotion(const Few& f, const Range& r, FewShared<NB>& sh)
             const float* vec = sh.tok[it % SLOTS];
             const float sw = sh.wsc[it % SLOTS][blk];
             const uint32_t t = tmem + buf * 2 * NB;
-            // CH columns per TMEM round trip (about 200 cycles whatever their number), the next chunk's
-            // in flight while this one's are scaled and added
-            constexpr int CH = NB < 32 ? NB : 32;
-            uint32_t pa[CH], pb[CH];
-            tmem_ld(t, pa);
+            // phase 2: the columns that have a scale.  The others' products are not added, not even times
+            // 0: an expert whose weights or scales hold a NaN or infinity spoils only its own tokens.
+            uint32_t takes = 0;
+            if (PHASE == 2) takes = __ballot_sync(0xffffffffu, lane < NB && vec[lane] != 0.0f);
+            uint32_t p[NB];
+            tmem_ld(t, p);
+            tmem_ld_wait(p);
 #pragma unroll
-            for (int c = 0; c < NB; c += CH) {
-                if (c >= f.Tp) break;
-                uint32_t (&p)[CH] = (c & CH) ? pb : pa;
-                uint32_t (&q)[CH] = (c & CH) ? pa : pb;
-                tmem_ld_wait(p);
-                if (c + CH < NB && c + CH < f.Tp) tmem_ld(t + c + CH, q);
-#pragma unroll
-                for (int i = 0; i < CH; i += 4) {
-                    const float4 x = *reinterpret_cast<const float4*>(vec + c + i);
+            for (int i = 0; i < NB; i += 4) {
+                const float4 x = *reinterpret_cast<const float4*>(vec + i);
+                if (PHASE == 1) {
                     float s0, s1, s2, s3;
                     fmul2(s0, s1, x.x, x.y, sw, sw);
                     fmul2(s2, s3, x.z, x.w, sw, sw);
-                    ffma2(acc[c + i], acc[c + i + 1], __uint_as_float(p[i]), __uint_as_float(p[i + 1]), s0, s1);
-                    ffma2(acc[c + i + 2], acc[c + i + 3], __uint_as_float(p[i + 2]), __uint_as_float(p[i + 3]), s2, s3);
+                    ffma2(acc[i], acc[i + 1], __uint_as_float(p[i]), __uint_as_float(p[i + 1]), s0, s1);
+                    ffma2(acc[i + 2], acc[i + 3], __uint_as_float(p[i + 2]), __uint_as_float(p[i + 3]), s2, s3);
+                } else {
+                    if ((takes >> i) & 1) acc[i] = fmaf(__uint_as_float(p[i]), x.x * sw, acc[i]);
+                    if ((takes >> i) & 2) acc[i + 1] = fmaf(__uint_as_float(p[i + 1]), x.y * sw, acc[i + 1]);
+                    if ((takes >> i) & 4) acc[i + 2] = fmaf(__uint_as_float(p[i + 2]), x.z * sw, acc[i + 2]);
+                    if ((takes >> i) & 8) acc[i + 3] = fmaf(__uint_as_float(p[i + 3]), x.w * sw, acc[i + 3]);
                 }
             }
             tc_fence_before();
@@ -605,11 +634,102 @@ __device__ void few_promotion(const Few& f, const Range& r, FewShared<NB>& sh)
                          (int64_t)blk * f.T * 128 + row;
 #pragma unroll
             for (int t = 0; t < NB; ++t)
-                if (PHASE == 1 ? (routed[t >> 5] >> (t & 31)) & 1 : t < f.T) __stcg(dst + t * 128, acc[t]);
+                if (PHASE == 1 ? (routed >> t) & 1 : t < f.T) __stcg(dst + t * 128, acc[t]);
         } else if (tile * 256 + (int64_t)tid < f.N) {
 #pragma unroll
             for (int t = 0; t < NB; ++t)
                 if (t < f.T) store_out(f, t, tile * 256 + (int64_t)tid, acc[t]);
+        }
+    }
+}
+
+// The promotion with tokens as the accumulator's rows: thread = token, and row block of the weights.
+template <int PHASE, int NB>
+__device__ void few_promotion_rows(const Few& f, const Range& r, FewShared<NB>& sh)
+{
+    static_assert(NB == 128, "a thread's 128 accumulators are a row block's columns");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int blk = warp >> 2, tok = tid & 127;
+    const uint32_t tmem = sh.tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + blk * NB;
+    uint32_t it = 0;
+    int seg = 0;
+    wait_previous();
+    Walk<PHASE> k(f, sh.experts.id, r);
+    for (; k.u < r.u1; ++seg) {
+        const uint32_t tile = k.tile, tile_u0 = k.u - k.kb;
+        // phase 1: only tokens routed to the tile's expert (gate weight not 0) matter, and their sums are
+        // stored without gaps
+        bool routed = tok < f.T;
+        int at = tok;
+        if (PHASE == 1) {
+            uint32_t word[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = 32 * i + lane;
+                word[i] = __ballot_sync(0xffffffffu, t < f.T && __ldcg(f.gate + (int64_t)k.e * f.Tp + t) != 0.0f);
+            }
+            at = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i == (warp & 3)) {
+                    routed = (word[i] >> lane) & 1;
+                    at += __popc(word[i] & ((1u << lane) - 1));
+                }
+                if (i < (warp & 3)) at += __popc(word[i]);
+            }
+        }
+        const uint32_t end = r.u1 < tile_u0 + r.per ? r.u1 : tile_u0 + r.per;
+        float acc[NB];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) acc[i] = 0.0f;
+#pragma unroll 1
+        for (; k.u < end; k.next(r.u1), ++it) {
+            const uint32_t buf = it & 1;
+            // the whole warp goes on or gives up (TMEM loads are warp-wide)
+            if (!__all_sync(0xffffffffu, mbar_wait(&sh.tfull[buf], (it >> 1) & 1, &sh.abort, f.timeout_ns))) return;
+            tc_fence_after();
+            const float x = sh.tok[it % SLOTS][tok], s = x * sh.wsc[it % SLOTS][blk];
+            // Phase 2: a token that did not pick the unit's expert has scale 0 here.  Its products are not
+            // added, not even times 0: an expert whose weights or scales hold a NaN or infinity spoils
+            // only its own tokens.
+            const bool on = routed && (PHASE == 1 || x != 0.0f);
+            if (__any_sync(0xffffffffu, on)) {
+                const uint32_t t = tmem + buf * 2 * NB;
+                constexpr int CH = 32;
+                uint32_t pa[CH], pb[CH];
+                tmem_ld(t, pa);
+#pragma unroll
+                for (int c = 0; c < NB; c += CH) {
+                    uint32_t (&p)[CH] = (c & CH) ? pb : pa;
+                    uint32_t (&q)[CH] = (c & CH) ? pa : pb;
+                    tmem_ld_wait(p);
+                    if (c + CH < NB) tmem_ld(t + c + CH, q);
+                    if (on)
+#pragma unroll
+                        for (int i = 0; i < CH; i += 2)
+                            ffma2(acc[c + i], acc[c + i + 1], __uint_as_float(p[i]), __uint_as_float(p[i + 1]), s, s);
+                    __syncwarp();
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.tempty[buf]);
+        }
+
+        const Parts p(f, r, tile_u0);
+        const bool shared = p.c1 > p.c0;
+        if (PHASE == 1 || shared) {
+            if (!routed) continue;
+            float* dst = (shared ? f.part + (2 * (int64_t)blockIdx.x + (seg ? 1 : 0)) * p.stride
+                                 : f.whole + (int64_t)tile * p.stride) +
+                         (int64_t)blk * f.T * 128 + at * 4;
+#pragma unroll
+            for (int i = 0; i < NB; i += 4)
+                __stcg(reinterpret_cast<float4*>(dst + i * f.T),
+                       make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]));
+        } else if (tok < f.T && tile * 256 + (int64_t)blk * 128 < f.N) {
+#pragma unroll
+            for (int i = 0; i < NB; i += 8) store_out8(f, tok, tile * 256 + (int64_t)(blk * 128 + i), acc + i);
         }
     }
 }
@@ -675,7 +795,10 @@ __global__ void __launch_bounds__(num_threads(NB), NB <= 16 ? 2 : 1)
         __syncwarp();
     } else {
         if (num_threads(NB) == 384) regs_inc<PROMO_REGS>();
-        few_promotion<PHASE, NB>(f, r, sh);
+        if constexpr (token_rows(NB))
+            few_promotion_rows<PHASE, NB>(f, r, sh);
+        else
+            few_promotion<PHASE, NB>(f, r, sh);
     }
     tc_fence_before();
     __syncthreads();
@@ -686,7 +809,7 @@ __global__ void __launch_bounds__(num_threads(NB), NB <= 16 ? 2 : 1)
                      : "memory");
 }
 
-// Block (tile of phase 1, 32 tokens): adds the tile's parts for the tokens routed to its expert, 8 at
+// Up to 32 tokens.  Block = tile of phase 1: adds its parts for the tokens routed to its expert, 8 at
 // a time, thread = channel; SwiGLU and 1x128 quantization.  Tokens not routed here (gate weight 0)
 // get zero rows of scale 0.  Everything but the parts is known (k_few_prep had completed before phase 1
 // let this kernel start), and done, before phase 1 ends.
@@ -700,10 +823,10 @@ __global__ void __launch_bounds__(128) k_few_act(const Few f, uint32_t ctas)
     const int tid = threadIdx.x, lane = tid & 31, w4 = tid >> 5;
     launch_dependents();
     const uint32_t J = (uint32_t)(f.I / 128), tile = blockIdx.x, a = tile / J, j = tile - a * J;
-    const int n_act = __ldcg(f.n_act), t0 = 32 * blockIdx.y;
+    const int n_act = __ldcg(f.n_act);
     const bool live = (int)a < n_act;
-    float gw = 0.0f;                          // gate weight of token t0 + lane
-    if (live && t0 + lane < f.T) gw = __ldcg(f.gate + (int64_t)__ldcg(f.act + a) * f.Tp + t0 + lane);
+    float gw = 0.0f;                          // gate weight of token `lane`
+    if (live && lane < f.T) gw = __ldcg(f.gate + (int64_t)__ldcg(f.act + a) * f.Tp + lane);
     const uint32_t routed = __ballot_sync(0xffffffffu, gw != 0.0f);
     if (tid < 32 && gw != 0.0f) tcol[__popc(routed & ((1u << lane) - 1))] = (uint8_t)lane;
     const int n = __popc(routed);
@@ -714,8 +837,8 @@ __global__ void __launch_bounds__(128) k_few_act(const Few f, uint32_t ctas)
         wait_previous();
         return;
     }
-    const int64_t row0 = (int64_t)a * f.Tp + t0;                     // of aq
-    float* const as = f.as + (int64_t)tile * f.Tp + t0;
+    const int64_t row0 = (int64_t)a * f.Tp;                          // of aq
+    float* const as = f.as + (int64_t)tile * f.Tp;
     uint8_t* const aq = f.aq + row0 * f.I + j * 128;
     const int i8 = lane & (ACT_TOKENS - 1);
     // A rehearsal of one round while phase 1 still runs, on numbers that are not used, fetches the
@@ -733,12 +856,13 @@ __global__ void __launch_bounds__(128) k_few_act(const Few f, uint32_t ctas)
         for (int i = 0; i < ACT_TOKENS; ++i) g[i] = u[i] = 0.0f;
 #pragma unroll 1
         for (uint32_t q = p.c0; q <= p.c1; ++q) {
-            int now = round;                  // (hidden again: no second copy of this loop either)
+            int now = round;                  // (hidden again, as is what follows from it: no second copy of this
+                                              // loop or of its loads either, which costs 4 us)
             asm volatile("" : "+r"(now));
-            const float* src = (p.c0 == p.c1 ? f.whole + (int64_t)tile * p.stride : p.at(q)) + (int64_t)t0 * 128 + tid;
+            const float* src = (p.c0 == p.c1 ? f.whole + (int64_t)tile * p.stride : p.at(q)) + tid;
             if (now < 0) src = f.gate;
-            const int64_t up = now < 0 ? 0 : (int64_t)f.T * 128;
-            const int mul = now < 0 ? 0 : 128;
+            int up = now < 0 ? 0 : f.T * 128, mul = now < 0 ? 0 : 128;
+            asm volatile("" : "+l"(src), "+r"(up), "+r"(mul));
             float x[2][ACT_TOKENS];           // all in flight at once; past the last column, one not used
 #pragma unroll
             for (int i = 0; i < ACT_TOKENS; ++i) {
@@ -777,10 +901,88 @@ __global__ void __launch_bounds__(128) k_few_act(const Few f, uint32_t ctas)
         // (the next round's writes of codes follow a barrier that these reads precede)
     }
     if (n == 0) wait_previous();
-    if (tid < 32 && t0 + lane < f.T && gw == 0.0f) as[lane] = 0.0f;
-    for (int i = tid; i < 32 * 8; i += 128)
-        if (t0 + (i >> 3) < f.T && !((routed >> (i >> 3)) & 1))
-            *reinterpret_cast<uint4*>(aq + (int64_t)(i >> 3) * f.I + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+    if (tid < 32 && lane < f.T && gw == 0.0f) as[lane] = 0.0f;
+}
+
+// The same behind few_promotion_rows, whose sums lie [channel / 4][token][4]: block = (tile of phase 1,
+// every second 32 of the tokens routed to its expert), thread = token and 32 channels, so that all lanes work and a
+// token's 64 values need no shuffle.  Codes of tokens not routed here are left as they are: phase 2 does
+// not add what it makes of them.
+__global__ void __launch_bounds__(128) k_few_act_rows(const Few f, uint32_t ctas)
+{
+    __shared__ float wmax[4][32], gcol[128];
+    __shared__ uint32_t words[4];
+    __shared__ uint8_t tcol[128];
+    const int tid = threadIdx.x, lane = tid & 31, w4 = tid >> 5;
+    launch_dependents();
+    const uint32_t J = (uint32_t)(f.I / 128), tile = blockIdx.x, a = tile / J, j = tile - a * J;
+    const int n_act = __ldcg(f.n_act), e = __ldcg(f.act + a);
+    const bool live = (int)a < n_act;
+    float gw = 0.0f;                          // gate weight of token tid
+    if (live && tid < f.T) gw = __ldcg(f.gate + (int64_t)e * f.Tp + tid);
+    const uint32_t word = __ballot_sync(0xffffffffu, gw != 0.0f);
+    if (lane == 0) words[w4] = word;
+    __syncthreads();
+    int n = 0, rank = __popc(word & ((1u << lane) - 1));
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        if (w < w4) rank += __popc(words[w]);
+        n += __popc(words[w]);
+    }
+    if (gw != 0.0f) {
+        tcol[rank] = (uint8_t)tid;
+        gcol[rank] = gw;
+    }
+    __syncthreads();
+    const Range r = few_range<1>(f, live ? n_act : 1, ctas);
+    const Parts p(f, r, (live ? tile : 0) * r.per);
+    wait_previous();
+    if (live && blockIdx.y == 0 && tid < f.T && gw == 0.0f) f.as[(int64_t)tile * f.Tp + tid] = 0.0f;
+#pragma unroll 1
+    for (int c0 = 32 * blockIdx.y; c0 < n; c0 += 32 * gridDim.y) {
+        const bool on = c0 + lane < n;
+        const int at = on ? c0 + lane : c0, t = tcol[at];
+        F2 g[16], u[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) g[i] = u[i] = f2(0.0f, 0.0f);
+#pragma unroll 1
+        for (uint32_t q = p.c0; q <= p.c1; ++q) {
+            const float* src = (p.c0 == p.c1 ? f.whole + (int64_t)tile * p.stride : p.at(q)) + w4 * 32 * f.T + at * 4;
+            float4 x[2][8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[0][i] = __ldcg(reinterpret_cast<const float4*>(src + 4 * i * f.T));
+                x[1][i] = __ldcg(reinterpret_cast<const float4*>(src + 4 * i * f.T + f.T * 128));
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                g[2 * i] = g[2 * i] + f2(x[0][i].x, x[0][i].y);
+                g[2 * i + 1] = g[2 * i + 1] + f2(x[0][i].z, x[0][i].w);
+                u[2 * i] = u[2 * i] + f2(x[1][i].x, x[1][i].y);
+                u[2 * i + 1] = u[2 * i + 1] + f2(x[1][i].z, x[1][i].w);
+            }
+        }
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            g[i] = g[i] * sigmoid2(g[i]) * u[i];
+            m = absmax3(m, lo(g[i]), hi(g[i]));
+        }
+        __syncthreads();                      // (the round before has read wmax)
+        wmax[w4][lane] = m;
+        __syncthreads();
+        const GroupScale gs =
+            group_scale(fmaxf(absmax3(wmax[0][lane], wmax[1][lane], wmax[2][lane]), wmax[3][lane]), f.mode);
+        if (!on) continue;
+        if (w4 == 0) f.as[(int64_t)tile * f.Tp + t] = gs.s * gcol[at];
+        uint32_t c[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            c[i] = encode4(lo(g[2 * i]), hi(g[2 * i]), lo(g[2 * i + 1]), hi(g[2 * i + 1]), gs.inv);
+        uint4* dst = reinterpret_cast<uint4*>(f.aq + ((int64_t)a * f.Tp + t) * f.I + j * 128 + w4 * 32);
+        dst[0] = make_uint4(c[0], c[1], c[2], c[3]);
+        dst[1] = make_uint4(c[4], c[5], c[6], c[7]);
+    }
 }
 
 // Output columns whose sums are in parts (the whole tiles are written already): block =
@@ -796,7 +998,8 @@ __global__ void __launch_bounds__(256) k_few_out(const Few f, uint32_t ctas)
     const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const Range r = few_range<2>(f, n_act ? n_act : 1, ctas);
     const Parts p(f, r, blockIdx.x * r.per);
-    const int64_t at = (int64_t)blk * f.T * 128 + (int64_t)t0 * 128 + row;
+    const int step = sum_step(f);
+    const int64_t at = (int64_t)blk * f.T * 128 + t0 * step + sum_at(f, row);
     wait_previous();
     if (n >= f.N || (n_act && p.c0 == p.c1)) return;
     float v[OUT_TOKENS];
@@ -810,7 +1013,7 @@ __global__ void __launch_bounds__(256) k_few_out(const Few f, uint32_t ctas)
             for (int q = 0; q < OUT_PARTS; ++q) {
                 const float* src = p.at(c + q <= p.c1 ? c + q : p.c1) + at;
 #pragma unroll
-                for (int i = 0; i < OUT_TOKENS; ++i) x[q][i] = __ldcg(src + (t0 + i < f.T ? i * 128 : 0));
+                for (int i = 0; i < OUT_TOKENS; ++i) x[q][i] = __ldcg(src + (t0 + i < f.T ? i * step : 0));
             }
 #pragma unroll
             for (int q = 0; q < OUT_PARTS; ++q)
@@ -861,10 +1064,11 @@ int launch_few_gemms(const Few& f, const CUtensorMap& tmW13, const CUtensorMap& 
     if (cudaLaunchKernelEx(&cfg, k_few_gemm<1, NB>, tmW13, tmX, tmW2, f) != cudaSuccess) return FP8_ERR_LAUNCH;
     const int64_t A = (int64_t)f.T * f.k < f.G ? (int64_t)f.T * f.k : f.G;
     cudaLaunchConfig_t act = cfg;
-    act.gridDim = dim3((unsigned)(A * (f.I / 128)), (unsigned)((f.T + 31) / 32), 1);
+    act.gridDim = dim3((unsigned)(A * (f.I / 128)), token_rows(NB) ? 2u : 1u, 1);
     act.blockDim = dim3(128, 1, 1);
     act.dynamicSmemBytes = 0;
-    if (cudaLaunchKernelEx(&act, k_few_act, f, (uint32_t)ctas) != cudaSuccess) return FP8_ERR_LAUNCH;
+    if (cudaLaunchKernelEx(&act, token_rows(NB) ? k_few_act_rows : k_few_act, f, (uint32_t)ctas) != cudaSuccess)
+        return FP8_ERR_LAUNCH;
     if (cudaLaunchKernelEx(&cfg, k_few_gemm<2, NB>, tmW2, tmA, tmW2, f) != cudaSuccess) return FP8_ERR_LAUNCH;
     cfg.gridDim = dim3((unsigned)((f.N + 255) / 256), (unsigned)((f.T + OUT_TOKENS - 1) / OUT_TOKENS), 1);
     cfg.blockDim = dim3(256, 1, 1);
@@ -918,8 +1122,7 @@ int launch_moe_mlp_few(const void* x, int in_dtype, int64_t T, int64_t K, int64_
     const int sms = device_sm_count();
     const unsigned ctas = (unsigned)(sms < 1 ? 1 : (sms < kFewMaxCtas ? sms : kFewMaxCtas));
     if (f.Tp <= 16) return launch_few_gemms<16>(f, tmW13, tmW2, tmX, tmA, ctas, st);
-    if (f.Tp <= 32) return launch_few_gemms<32>(f, tmW13, tmW2, tmX, tmA, ctas, st);
-    if (f.Tp <= 64) return launch_few_gemms<64>(f, tmW13, tmW2, tmX, tmA, ctas, st);
+    if (f.Tp <= MAX_COLUMN_TOKENS) return launch_few_gemms<32>(f, tmW13, tmW2, tmX, tmA, ctas, st);
     return launch_few_gemms<128>(f, tmW13, tmW2, tmX, tmA, ctas, st);
 }
 

@@ -176,3 +176,63 @@ def test_captured_and_replayed_beside_another_call():
 def test_no_tokens():
     case = _case(0, 2, 4, 256, 128, 256, seed=1)
     assert _run(case).shape == (0, 256)
+
+
+@pytest.mark.parametrize("T", [5, 32, 33, 128])
+def test_a_bad_expert_spoils_only_its_tokens(T):
+    """NaN codes and infinite scales of one expert's weights reach the tokens routed to it, no other:
+    though every expert's products are made with every token."""
+    G, e = 6, 2
+    case = list(_case(T, 2, G, 256, 256, 384, seed=T))
+    case[1][0] = [e, 5]                           # picked by one token at least,
+    case[1][T - 1] = [0, 1]                       # and not by all
+    ref = _run(case)
+    hit = torch.from_numpy((case[1] == e).any(1)).to(dev())
+    assert bool(hit.any()) and not bool(hit.all())
+    for i, bad in ((3, 0x7F), (4, np.inf), (5, 0x7F), (5, 0xFF), (6, np.inf), (6, np.nan)):
+        spoilt = list(case)
+        spoilt[i] = case[i].copy()
+        spoilt[i][e] = bad
+        got = _run(spoilt)
+        assert torch.equal(got[~hit], ref[~hit]), i
+        assert not bool(torch.isfinite(got[hit]).any()), i
+    assert fg.fp8_get_status() == fg.FP8_OK
+
+
+@pytest.mark.parametrize("T,out", [(3, torch.bfloat16), (40, torch.float32), (128, torch.bfloat16)])
+def test_many_output_columns(T, out):
+    """More output tiles than CTAs: whole tiles are rounded and stored by the CTA that added them up."""
+    case = _case(T, 2, 3, 128, 128, 128 * 601, seed=T)
+    got = _run(case, out)
+    _check(got, case)
+    assert torch.equal(got, _run(case, out))
+
+
+@pytest.mark.parametrize("T", [2, 33])
+def test_most_experts_and_picks(T):
+    """1024 experts, 128 picks a token."""
+    case = _case(T, 128, 1024, 128, 128, 128, seed=T)
+    _check(_run(case), case)
+    assert fg.fp8_get_status() == fg.FP8_OK
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_weights_past_32_bit_offsets(T):
+    """Experts whose weights lie past 2^32 bytes give the bits of the same experts side by side."""
+    G, K, I, N = 400, synth.HIDDEN, 1024, synth.HIDDEN
+    pick = [0, 250, G - 1]
+    x, _, _, w13, s13, w2, s2 = _case(T, 1, len(pick), K, I, N, seed=T)
+    assert (pick[1] + 1) * 2 * I * K > 2 ** 31 and pick[2] * 2 * I * K > 2 ** 32
+    topk = np.stack([np.arange(3, dtype=np.int32)] * T)
+    w = np.random.default_rng(T).uniform(0.1, 1.0, topk.shape).astype(np.float32)
+    near = _run((x, topk, w, w13, s13, w2, s2))
+    far = []
+    for a in (w13, s13, w2, s2):
+        t = torch.empty((G,) + a.shape[1:], dtype=torch.uint8 if a.dtype == np.uint8 else torch.float32, device=dev())
+        t.fill_(0x7F if a.dtype == np.uint8 else float("nan"))
+        for i, e in enumerate(pick):
+            t[e] = to_dev(a[i])
+        far.append(t)
+    got = fg.moe_mlp_few(x.to(dev()), to_dev(np.array(pick, np.int32)[topk]), to_dev(w), *far)
+    assert torch.equal(got, near)
+    assert fg.fp8_get_status() == fg.FP8_OK
