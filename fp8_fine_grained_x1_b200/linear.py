@@ -397,7 +397,10 @@ class MoeMlpStep:
     Up to MOE_FEW_MAX_TOKENS tokens take one call that reads each active
     expert's weights once (fp8_moe_mlp_few).  More tokens are quantized and
     dispatched to 128-padded groups, and the SwiGLU between the two grouped GEMMs
-    quantizes the rows in use for the second; H is BF16 there and FP32 in the few-token form.  `few`
+    quantizes the rows in use for the second; H is BF16 there and FP32 in the
+    few-token form.  On 32 experts of 7168 x 2048, top-8, the few-token form took
+    70, 196, 240, 249 and 275 us for 1, 8, 32, 64 and 128 tokens, the dispatched
+    form 177, 389, 461, 496 and 512: it is taken wherever it can be.  `few`
     overrides the choice."""
 
     def __init__(self, x, topk, weights, qw13, sw13, qw2, sw2, out_dtype=torch.bfloat16, scale_mode=SCALE_FP32,

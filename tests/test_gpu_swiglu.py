@@ -218,6 +218,29 @@ def test_backward_rows_in_use():
                         ERR * np.abs(a[:blocks]), fg.SCALE_FP32)
 
 
+@pytest.mark.parametrize("mode", [fg.SCALE_FP32, fg.SCALE_POW2])
+def test_gates_far_below_zero(mode):
+    """Whole groups of gates between -85 and -16, where exp(-g) is large.  exp(-g) is 2^(g * -log2(e)) with the
+    product and the constant rounded to FP32: half a step of the exponent each at most, |g| * 2^-23 of the
+    sigmoid together, beside the other errors."""
+    M, I = 256, 256
+    rng = np.random.default_rng(21)
+    h = np.concatenate((rng.uniform(-85.0, -16.0, (M, I)), rng.normal(0, 1e18, (M, I))), 1).astype(np.float32)
+    x, val = _input(h, "fp32")
+    qa, sa, qh, sh = fg.swiglu_quant(x, True, mode)
+    a = mlp.swiglu(val)
+    _check_rows(_np(qa), _np(sa), a, (ERR + np.abs(val[:, :I]) * 2.0 ** -23) * np.abs(a), mode)
+    back = mlp.decode_1x128(_np(qh), _np(sh))
+    da, dv = _input(_da(M, I, 9), "fp32")
+    out = fg.swiglu_bwd(qh, sh, da, ("qdh", "qdhT", "qaT"), mode)
+    dh, mag = mlp.swiglu_grads(back, dv)
+    a, g = mlp.swiglu(back), np.abs(back[:, :I])
+    err = (ERR + np.concatenate((g, g), 1) * 2.0 ** -23) * mag
+    _check_rows(_np(out["qdh"]), _np(out["sdh"]), dh, err, mode)
+    _check_cols(_np(out["qdhT"]), _np(out["sdhT"]), dh, err, mode)
+    _check_cols(_np(out["qaT"]), _np(out["saT"]), a, (ERR + g * 2.0 ** -23) * np.abs(a), mode)
+
+
 def test_strided_outputs():
     """Codes written into slices of wider buffers, the rest of them untouched."""
     M, I = 128, 256
