@@ -342,8 +342,10 @@ class GatedMlpStep:
         self.inputs, self.output = [x, w13, w2], self.y
         self._fork = _Fork(d)
         self._grad = None
+        self._ran = False
 
     def __call__(self, stream=None):
+        self._ran = True
         cur, side = self._fork.begin(stream)
         fp8_quant_w_128x128(self.w13, self.qw13, self.sw13, self.mode, side)
         fp8_quant_w_128x128(self.w2, self.qw2, self.sw2, self.mode, side)
@@ -373,6 +375,11 @@ class GatedMlpStep:
         return self._grad
 
     def backward(self, dy, stream=None):
+        if not self._ran:
+            raise RuntimeError("backward needs a forward pass before it")
+        if dy.shape != self.y.shape or dy.device != self.y.device:
+            raise ValueError(f"dy must have y's shape {tuple(self.y.shape)} and device {self.y.device}, "
+                             f"got {tuple(dy.shape)} on {dy.device}")
         g = self._gradient_buffers()
         cur, side = self._fork.begin(stream)
         # dy along tokens and x's cached codes regrouped, for the two Wgrads

@@ -372,7 +372,7 @@ int fp8_moe_combine(const void* D, int d_dtype, int64_t M_cap, int64_t N, const 
  *        memory, e.g. group_offsets + G of a dispatch; clamped to [0, M].  Rows
  *        at or beyond it do not matter and are not written, nor are their scales.
  * silu and the products are FP32 and a is not rounded before its quantization.
- * Inputs are finite, and so is a.
+ * Inputs are finite, and so is a; what is not spoils the 1x128 groups it lies in.
  * Sizes: M >= 0 (0 launches nothing), I > 0, I % 128 == 0, 2I <= 2^31 - 1;
  * ldh, ldqh >= 2I, ldqa >= I.  n_rows 4-byte aligned.  One kernel launch.
  */
@@ -431,7 +431,9 @@ int fp8_swiglu_bwd(const uint8_t* qh, int64_t ldqh, const float* sh, const void*
  *   workspace  caller-owned device scratch of fp8_moe_mlp_few_workspace_bytes
  *           bytes, 256-byte aligned, contents on entry ignored; calls that may
  *           overlap (other streams, captured graphs that run at once) need one each
- * The sums are taken in a fixed order: equal inputs give equal bits.
+ * The sums are taken in a fixed order: equal inputs give equal bits.  What is not
+ * finite stays with its token, or, in an expert's weights or scales, with the
+ * tokens routed to that expert.
  * Sizes: 0 <= T <= FP8_MOE_FEW_MAX_TOKENS (0 launches nothing), 1 <= k <= 128,
  * 1 <= G <= 1024; K, I, N > 0 and multiples of 128; G*2I, G*N <= 2^31 - 1;
  * ldx >= K, ldo >= N.  x, W13, W2 and out 16-byte aligned.  Five kernel launches.

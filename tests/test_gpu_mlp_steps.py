@@ -187,3 +187,17 @@ def test_moe_mlp_refusals():
     x = torch.zeros((128, 256), dtype=torch.bfloat16, device=dev())
     with pytest.raises(ValueError, match="fit"):
         linear.GatedMlpStep(x, torch.zeros((256, 128), device=dev()), torch.zeros((256, 128), device=dev()))
+
+
+def test_gated_mlp_backward_refusals():
+    x = torch.zeros((128, 256), dtype=torch.bfloat16, device=dev())
+    step = linear.GatedMlpStep(x, torch.zeros((256, 256), device=dev()), torch.zeros((384, 128), device=dev()))
+    dy = torch.zeros((128, 384), dtype=torch.bfloat16, device=dev())
+    with pytest.raises(RuntimeError, match="forward"):
+        step.backward(dy)
+    step()
+    for bad in (dy[:64], dy[:, :256], torch.zeros((256, 384), dtype=torch.bfloat16, device=dev()), dy.cpu()):
+        with pytest.raises(ValueError, match="dy"):
+            step.backward(bad)
+    assert all(bool((g == 0).all()) for g in step.backward(dy))
+    assert fg.fp8_get_status() == fg.FP8_OK

@@ -241,6 +241,38 @@ def test_gates_far_below_zero(mode):
     _check_cols(_np(out["qaT"]), _np(out["saT"]), a, (ERR + g * 2.0 ** -23) * np.abs(a), mode)
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_what_is_not_finite_stays_in_its_groups(bad):
+    M, I = 256, 384
+    x, _ = _input(_h(M, I, 31), "bf16")
+    ref = fg.swiglu_quant(x)
+    y = x.clone()
+    y[70, 130] = bad                      # a gate of the second channel block
+    y[71, I + 3] = bad                    # an up value of the first
+    got = fg.swiglu_quant(y)
+    for codes, scales, width in ((0, 1, I // 128), (2, 3, 2 * I // 128)):
+        same = torch.ones((M, width), dtype=torch.bool, device=dev())
+        same[70, 1] = False
+        same[71, 0 if codes == 0 else I // 128] = False
+        assert torch.equal(got[codes].view(M, width, 128)[same], ref[codes].view(M, width, 128)[same])
+        assert torch.equal(got[scales].t()[same], ref[scales].t()[same])
+    da, _ = _input(_da(M, I, 10), "bf16")
+    back = fg.swiglu_bwd(ref[2], ref[3], da)
+    sh = ref[3].clone()
+    sh[1, 70] = bad
+    out = fg.swiglu_bwd(ref[2], sh, da)
+    same = torch.ones((M, 2 * I // 128), dtype=torch.bool, device=dev())
+    same[70, [1, 1 + I // 128]] = False
+    assert torch.equal(out["qdh"].view(M, -1, 128)[same], back["qdh"].view(M, -1, 128)[same])
+    assert torch.equal(out["sdh"].t()[same], back["sdh"].t()[same])
+    # the other 128 tokens' and the other channels' groups along tokens
+    ch = torch.ones(2 * I, dtype=torch.bool, device=dev())
+    ch[128:256] = ch[I + 128:I + 256] = False
+    assert torch.equal(out["qdhT"][:, 128:], back["qdhT"][:, 128:]) and torch.equal(out["qdhT"][ch], back["qdhT"][ch])
+    assert torch.equal(out["qaT"][:, 128:], back["qaT"][:, 128:]) and torch.equal(out["qaT"][ch[:I]], back["qaT"][ch[:I]])
+    assert fg.fp8_get_status() == fg.FP8_OK
+
+
 def test_strided_outputs():
     """Codes written into slices of wider buffers, the rest of them untouched."""
     M, I = 128, 256
