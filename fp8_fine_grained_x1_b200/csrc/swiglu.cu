@@ -310,7 +310,7 @@ __device__ __forceinline__ void cp_arrive(uint64_t* bar)
 // Persistent CTAs of 512 threads over tiles of 128 tokens x 128 channels of I (channel
 // block fastest), which arrive by cp.async while the tile before is worked on: into the other of two
 // stages, or, with FP32 gradients, into the only one once its values are in registers.  (Three TMA
-// boxes instead save a tenth of the instructions, yet the kernel took 645 us instead of 534 for
+// boxes instead save a tenth of the instructions, yet the kernel took 645 us instead of 534 then for
 // 135168 x 2048.)
 // Warp w owns tokens 8w .. 8w+7, lane l channels 4l .. 4l+3, so a warp holds whole 1x128
 // groups (one warp reduction each; lane j derives the scale of group j of the warp's 16 once)
@@ -320,8 +320,11 @@ __device__ __forceinline__ void cp_arrive(uint64_t* bar)
 // lane: two wavefronts per store) and leave as whole 128-byte rows.
 // The 16 warps never stop at a common barrier: each of a tile's three hand-overs (part, inv,
 // outT) is an mbarrier that a warp arrives on, does work that does not need it, and
-// then waits for -- the rows of the tile before go out between part and inv, the 1x128 groups
-// are encoded between inv and outT.
+// then waits for -- the rows of the tile before go out and the 1x128 groups get their scales
+// between part and inv, the 1x128 groups are encoded between inv and outT.  The order counts:
+// 4096 x 9216 took 74 us, 77 with the 1x128 scales behind the channels', 86 with them or the next
+// tile's loads before the tile before's rows, 87 and 93 with half or all of the 1x128 codes before
+// the channels' scales.  (Waits that suspend instead of spinning: 1 % more.)
 // Tokens at or beyond the rows in use count as zero in the 128x1 groups.
 template <typename Tda>
 __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p)
@@ -349,7 +352,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
 
     // A wait that runs out is reported, and what this launch writes from then on is worthless.
     auto wait = [&](uint64_t* bar, int parity) {
-        mbar_wait(bar, (uint32_t)parity & 1u, &s.abort, p.timeout_ns);
+        mbar_wait_spin(bar, (uint32_t)parity & 1u, &s.abort, p.timeout_ns);
         __syncwarp();
     };
     auto arrive = [&](uint64_t* bar) {
@@ -488,6 +491,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
             wait(&s.bOut, it - 1);
             store_rows(prev);
         }
+        // maxima and scales of the 1x128 groups (lane j: group j of the warp's 16), while others get here
+        GroupScale gs{};
+        if (p.qdh) {
+#pragma unroll
+            for (int i = 0; i < kBwdTok; ++i)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const F2 (&r)[2] = v[x][i];
+                    const float m = warp_absmax(absmax4(lo(r[0]), hi(r[0]), lo(r[1]), hi(r[1])));
+                    if (lane == 0) s.rmax[w][8 * x + i] = m;
+                }
+            __syncwarp();
+            gs = group_scale(s.rmax[w][lane & 15], p.mode);
+            __syncwarp();
+        }
         wait(&s.bPart, it);
         if (NST == 1 && next.tb < ntb) load(next, 0);
         if (wantT) {
@@ -521,17 +539,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
                             make_uint2(pack_bf16(v[x][i][0]), pack_bf16(v[x][i][1]));
         }
         if (p.qdh) {
-#pragma unroll
-            for (int i = 0; i < kBwdTok; ++i)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const F2 (&r)[2] = v[x][i];
-                    const float m = warp_absmax(absmax4(lo(r[0]), hi(r[0]), lo(r[1]), hi(r[1])));
-                    if (lane == 0) s.rmax[w][8 * x + i] = m;
-                }
-            __syncwarp();
-            const GroupScale gs = group_scale(s.rmax[w][lane & 15], p.mode);
-            __syncwarp();
             if (lane < 16 && (lane & 7) < nr)
                 p.sdh[(int64_t)((lane >> 3) * ncb + tile.cb) * p.M + tw + (lane & 7)] = gs.s;
             uint8_t* dst = p.qdh + tw * p.ldqdh + col;
