@@ -96,11 +96,14 @@ __device__ __forceinline__ uint32_t scale_cvt4(F2 a, F2 b, float inv)
 
 // ------------------------------------------------------------ forward
 
-// Rows per lane, and CTAs per SM (which caps the registers at 80): of 1 and 2 rows with 2 to 5
-// CTAs, 2 and 3 ran fastest (135168 x 2048: 322 us; the others 355 to 419).
+// Threads of a CTA, rows per lane, and CTAs per SM (which caps the registers at 80): of 1 to 4 rows
+// and 64 to 256 threads these ran fastest over the range of sizes (4096 x 9216: 45.3 us, 135168 x 2048:
+// 305; 256 threads 46.8 and 315; 3 rows and 5 CTAs 45.5 and 300, but 3.9 us instead of 2.9 for 7 x 512;
+// others 47 to 54 and 315 to 358).
+constexpr int kFwdThreads = 128;
 constexpr int kFwdSteps = 2;
-constexpr int kFwdCtasPerSm = 3;
-constexpr int kFwdRowsPerCta = 32 * kFwdSteps;   // 8 warps x 4 rows x steps
+constexpr int kFwdCtasPerSm = 6;
+constexpr int kFwdRowsPerCta = kFwdThreads / 8 * kFwdSteps;   // 8 lanes a row
 
 // Lane l of a row's 8 lanes owns 16 of a group's 128 channels, in 16-byte pieces 128 bytes
 // apart (so that the 8 lanes of a row read 128 contiguous bytes at a time): BF16 2 pieces of 8
@@ -168,7 +171,7 @@ __device__ __forceinline__ void encode16(const F2 (&v)[8], float inv, uint32_t (
     for (int i = 0; i < 4; ++i) c[i] = scale_cvt4(v[2 * i], v[2 * i + 1], inv);
 }
 
-// CTA = 256 threads = 8 warps; 8 lanes own the 128 gate and the 128 up channels of one
+// CTA = 4 warps; 8 lanes own the 128 gate and the 128 up channels of one
 // channel block of a row (16 + 16 a lane), so a warp works on 4 rows at once and each
 // of a row's three groups (a, g, u) reduces its max-abs in three shuffles.  Lane 0 of
 // the row then derives the scale of a, lane 1 that of g, lane 2 that of u, in the same
@@ -177,24 +180,23 @@ __device__ __forceinline__ void encode16(const F2 (&v)[8], float inv, uint32_t (
 // Grid (1-D): channel block fastest, then row blocks, so adjacent CTAs read adjacent
 // segments of the same rows.
 template <typename Tin, bool KEEP>
-__global__ void __launch_bounds__(256, kFwdCtasPerSm) k_swiglu_quant(
-    const Tin* __restrict__ h, int64_t M, int64_t I, int64_t ldh, uint8_t* __restrict__ qa,
-    int64_t ldqa, float* __restrict__ sa, uint8_t* __restrict__ qh, int64_t ldqh,
-    float* __restrict__ sh, const int32_t* __restrict__ n_rows, int mode)
+__global__ void __launch_bounds__(kFwdThreads, kFwdCtasPerSm) k_swiglu_quant(
+    const Tin* __restrict__ h, int M, int I, int ldh, uint8_t* __restrict__ qa, int ldqa,
+    float* __restrict__ sa, uint8_t* __restrict__ qh, int ldqh, float* __restrict__ sh,
+    const int32_t* __restrict__ n_rows, int mode)
 {
     using V = Sixteen<Tin>;
     const int l = threadIdx.x & 7;
-    const int64_t ncb = I / 128;
-    const int64_t cb = blockIdx.x % ncb;
-    const int64_t m0 = (int64_t)(blockIdx.x / ncb) * kFwdRowsPerCta + (threadIdx.x >> 3);
-    const int64_t rows = live_rows(n_rows, M);
-    const int64_t col = cb * 128 + l * V::kPer;
+    const uint32_t ncb = (uint32_t)I / 128, rb = blockIdx.x / ncb, cb = blockIdx.x - rb * ncb;
+    const uint32_t m0 = rb * kFwdRowsPerCta + (threadIdx.x >> 3);    // may pass 2^31 by less than a CTA's rows
+    const uint32_t rows = (uint32_t)live_rows(n_rows, M);
+    const int col = (int)cb * 128 + l * V::kPer;
 
     V rg[kFwdSteps], ru[kFwdSteps];
 #pragma unroll
     for (int i = 0; i < kFwdSteps; ++i) {
-        const int64_t m = m0 + 32 * i;
-        const Tin* src = h + (m < rows ? m : 0) * ldh + col;
+        const uint32_t m = m0 + kFwdThreads / 8 * i;
+        const Tin* src = h + (int64_t)(int)(m < rows ? m : 0) * ldh + col;
 #pragma unroll
         for (int j = 0; j < V::kPieces; ++j) {
             rg[i].r[j] = ru[i].r[j] = make_uint4(0, 0, 0, 0);
@@ -206,7 +208,7 @@ __global__ void __launch_bounds__(256, kFwdCtasPerSm) k_swiglu_quant(
     }
 #pragma unroll
     for (int i = 0; i < kFwdSteps; ++i) {
-        const int64_t m = m0 + 32 * i;
+        const uint32_t m = m0 + kFwdThreads / 8 * i;
         const bool live = m < rows;
         F2 g[8], u[8], a[8];
         rg[i].get(g);
@@ -220,13 +222,13 @@ __global__ void __launch_bounds__(256, kFwdCtasPerSm) k_swiglu_quant(
         }
         const GroupScale gs = group_scale(mine, mode);
         if (live && l < (KEEP ? 3 : 1))
-            (l == 0 ? sa + cb * M : sh + (l == 1 ? cb : ncb + cb) * M)[m] = gs.s;
+            (l == 0 ? sa + (int64_t)(int)cb * M : sh + (int64_t)(int)(l == 1 ? cb : ncb + cb) * M)[m] = gs.s;
         uint32_t c[4];
         encode16(a, __shfl_sync(0xffffffffu, gs.inv, 0, 8), c);
-        if (live) V::store(qa + m * ldqa + col, c);
+        if (live) V::store(qa + (int64_t)(int)m * ldqa + col, c);
         if (KEEP) {
             const float ig = __shfl_sync(0xffffffffu, gs.inv, 1, 8), iu = __shfl_sync(0xffffffffu, gs.inv, 2, 8);
-            uint8_t* dst = qh + m * ldqh + col;
+            uint8_t* dst = qh + (int64_t)(int)m * ldqh + col;
             encode16(g, ig, c);
             if (live) V::store(dst, c);
             encode16(u, iu, c);
@@ -249,7 +251,7 @@ struct BwdParams {
     uint8_t* qaT;
     float* saT;
     const int32_t* n_rows;
-    int64_t M, I, ldqh, ldda, lddh, ldqdh, ldqdhT, ldqaT;
+    int M, I, ldqh, ldda, lddh, ldqdh, ldqdhT, ldqaT;
     int mode;
     uint64_t timeout_ns;
 };
@@ -322,7 +324,7 @@ __device__ __forceinline__ void cp_arrive(uint64_t* bar)
 // outT) is an mbarrier that a warp arrives on, does work that does not need it, and
 // then waits for -- the rows of the tile before go out and the 1x128 groups get their scales
 // between part and inv, the 1x128 groups are encoded between inv and outT.  The order counts:
-// 4096 x 9216 took 74 us, 77 with the 1x128 scales behind the channels', 86 with them or the next
+// 4096 x 9216 took 74 us (72 since, by 32-bit offsets), 77 with the 1x128 scales behind the channels', 86 with them or the next
 // tile's loads before the tile before's rows, 87 and 93 with half or all of the 1x128 codes before
 // the channels' scales.  (Waits that suspend instead of spinning: 1 % more.)
 // Tokens at or beyond the rows in use count as zero in the 128x1 groups.
@@ -334,9 +336,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
     constexpr int NST = kBwdStages<Tda>;
     const int w = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int32_t ncb = (int32_t)(p.I / 128);
-    const int64_t rows = live_rows(p.n_rows, p.M);
-    const int32_t ntb = (int32_t)((rows + 127) / 128);
+    const int32_t ncb = p.I / 128;
+    const int rows = (int)live_rows(p.n_rows, p.M);
+    const int32_t ntb = (int32_t)(((uint32_t)rows + 127) / 128);
     const bool wantH = p.qdhT != nullptr, wantA = p.qaT != nullptr, wantT = wantH || wantA;
 
     if (threadIdx.x == 0) {
@@ -365,50 +367,50 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
     const int64_t offQ = (int64_t)(threadIdx.x >> 3) * p.ldqh + (threadIdx.x & 7) * 16;
     const int64_t offD = (int64_t)(threadIdx.x / kPerRow) * p.ldda + threadIdx.x % kPerRow * kPer;
     auto load = [&](Tile tile, int st) {
-        const int64_t cb = tile.cb, t0 = (int64_t)tile.tb * 128;
-        const uint8_t* q = p.qh + t0 * p.ldqh + cb * 128 + offQ;
-        const Tda* da = static_cast<const Tda*>(p.da) + t0 * p.ldda + cb * 128 + offD;
+        const int t0 = tile.tb * 128;
+        const uint8_t* q = p.qh + (int64_t)t0 * p.ldqh + tile.cb * 128 + offQ;
+        const Tda* da = static_cast<const Tda*>(p.da) + (int64_t)t0 * p.ldda + tile.cb * 128 + offD;
         const uint32_t dst = smem_u32(&s.stage[st]) + threadIdx.x * 16;
         constexpr uint32_t kU = offsetof(BwdStage<Tda>, u), kD = offsetof(BwdStage<Tda>, da), kStep = kBwdThreads * 16;
-        if (t0 + 128 <= rows) {
+        if (t0 <= rows - 128) {
             cp16(dst, q);
             cp16(dst + kU, q + p.I);
-            q += 64 * p.ldqh;
+            q += (int64_t)64 * p.ldqh;
             cp16(dst + kStep, q);
             cp16(dst + kU + kStep, q + p.I);
 #pragma unroll
-            for (int i = 0; i < 128 / kStepD; ++i, da += kStepD * p.ldda) cp16(dst + kD + i * kStep, da);
+            for (int i = 0; i < 128 / kStepD; ++i, da += (int64_t)kStepD * p.ldda) cp16(dst + kD + i * kStep, da);
         } else {
             for (int i = 0; i < 2; ++i) {
-                const int64_t r = (threadIdx.x >> 3) + 64 * i;
-                const bool live = t0 + r < rows;
-                const uint8_t* src = live ? q + i * 64 * p.ldqh : p.qh;
+                const int r = (threadIdx.x >> 3) + 64 * i;
+                const bool live = t0 < rows - r;
+                const uint8_t* src = live ? q + (int64_t)(i * 64) * p.ldqh : p.qh;
                 cp16(dst + i * kStep, src, live);
                 cp16(dst + kU + i * kStep, src + p.I, live);
             }
             for (int i = 0; i < 128 / kStepD; ++i) {
-                const bool live = t0 + threadIdx.x / kPerRow + i * kStepD < rows;
-                cp16(dst + kD + i * kStep, live ? da + i * kStepD * p.ldda : static_cast<const Tda*>(p.da), live);
+                const bool live = t0 < rows - (int)(threadIdx.x / kPerRow) - i * kStepD;
+                cp16(dst + kD + i * kStep, live ? da + (int64_t)(i * kStepD) * p.ldda : static_cast<const Tda*>(p.da), live);
             }
         }
         cp_arrive(&s.full[st]);
     };
     // the checkpoint scale of this lane's (half, token): lanes 0-7 the gate's, 8-15 the up half's
     auto load_scale = [&](Tile tile) -> float {
-        const int64_t t = (int64_t)tile.tb * 128 + w * kBwdTok + (lane & 7);
-        return lane < 16 && t < rows ? __ldg(p.sh + (int64_t)((lane >> 3) * ncb + tile.cb) * p.M + t) : 0.0f;
+        const int t = tile.tb < ntb ? tile.tb * 128 + w * kBwdTok + (lane & 7) : p.M;
+        return lane < 16 && (uint32_t)t < (uint32_t)rows ? __ldg(p.sh + (int64_t)((lane >> 3) * ncb + tile.cb) * p.M + t) : 0.0f;
     };
     // whole 128-byte rows of a tile's transposed codes: 8 threads a row, 64 channels a pass
     auto store_rows = [&](Tile tile) {
-        const int64_t cb = tile.cb, t0 = (int64_t)tile.tb * 128;
+        const int t0 = tile.tb * 128;
 #pragma unroll
         for (int x = 0; x < 3; ++x) {
             if (!(x < 2 ? wantH : wantA)) continue;
-            const int64_t ld = x < 2 ? p.ldqdhT : p.ldqaT;
-            uint8_t* dst = (x < 2 ? p.qdhT + (x * p.I + cb * 128) * ld : p.qaT + cb * 128 * ld) + t0 +
-                           (threadIdx.x >> 3) * ld + (threadIdx.x & 7) * 16;
+            const int ld = x < 2 ? p.ldqdhT : p.ldqaT;
+            const int row = (x < 2 ? x * p.I : 0) + tile.cb * 128 + (int)(threadIdx.x >> 3);
+            uint8_t* dst = (x < 2 ? p.qdhT : p.qaT) + (int64_t)row * ld + t0 + (threadIdx.x & 7) * 16;
 #pragma unroll
-            for (int i = 0; i < 2; ++i, dst += 64 * ld) {
+            for (int i = 0; i < 2; ++i, dst += (int64_t)64 * ld) {
                 const int c = (threadIdx.x >> 3) + 64 * i;
                 const int wl = c >> 2;                                // lane that wrote channel c
                 uint4 q = *reinterpret_cast<const uint4*>(&s.outT[x][c * 128 + (((threadIdx.x & 7) ^ (wl & 7)) * 16)]);
@@ -438,10 +440,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
         const float scale_next = load_scale(next);
         wait(&s.full[st], NST == 2 ? it >> 1 : it);
 
-        const int64_t cb = tile.cb, t0 = (int64_t)tile.tb * 128;
-        const int64_t col = cb * 128 + 4 * lane;
-        const int64_t tw = t0 + w * kBwdTok;
-        const int nr = rows - tw < kBwdTok ? (int)(rows - tw) : kBwdTok;      // this warp's rows in use, may be <= 0
+        const int col = tile.cb * 128 + 4 * lane;
+        const int tw = tile.tb * 128 + w * kBwdTok;
+        const int nr = min((int64_t)rows - tw, (int64_t)kBwdTok);             // this warp's rows in use, may be <= 0
         F2 v[3][kBwdTok][2];      // dG, dU, a
         {
             const BwdStage<Tda>& d = s.stage[st];
@@ -518,18 +519,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
                 for (int k = 1; k < kBwdWarps - 1; k += 2) a = absmax3(a, s.part[x][k][c], s.part[x][k + 1][c]);
                 const GroupScale gs = group_scale(fmaxf(a, s.part[x][kBwdWarps - 1][c]), p.mode);
                 s.inv[threadIdx.x] = gs.inv;
-                const int64_t tb = tile.tb;
+                const int ch = tile.cb * 128 + c;
                 if (x < 2)
-                    p.sdhT[tb * 2 * p.I + x * p.I + cb * 128 + c] = gs.s;
+                    p.sdhT[(int64_t)tile.tb * (2 * p.I) + x * p.I + ch] = gs.s;
                 else
-                    p.saT[tb * p.I + cb * 128 + c] = gs.s;
+                    p.saT[(int64_t)tile.tb * p.I + ch] = gs.s;
             }
             arrive(&s.bInv);
         }
 
         // 1x128 groups and BF16 rows
         if (p.dh) {
-            __nv_bfloat16* dst = p.dh + tw * p.lddh + col;
+            __nv_bfloat16* dst = p.dh + (int64_t)tw * p.lddh + col;
 #pragma unroll
             for (int i = 0; i < kBwdTok; ++i, dst += p.lddh)
 #pragma unroll
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
         if (p.qdh) {
             if (lane < 16 && (lane & 7) < nr)
                 p.sdh[(int64_t)((lane >> 3) * ncb + tile.cb) * p.M + tw + (lane & 7)] = gs.s;
-            uint8_t* dst = p.qdh + tw * p.ldqdh + col;
+            uint8_t* dst = p.qdh + (int64_t)tw * p.ldqdh + col;
 #pragma unroll
             for (int i = 0; i < kBwdTok; ++i, dst += p.ldqdh)
 #pragma unroll
@@ -611,9 +612,11 @@ cudaError_t fwd(const void* h, int64_t M, int64_t I, int64_t ldh, uint8_t* qa, i
     const unsigned grid = (unsigned)((M + kFwdRowsPerCta - 1) / kFwdRowsPerCta * (I / 128));
     const Tin* x = static_cast<const Tin*>(h);
     if (qh)
-        k_swiglu_quant<Tin, true><<<grid, 256, 0, st>>>(x, M, I, ldh, qa, ldqa, sa, qh, ldqh, sh, n_rows, mode);
+        k_swiglu_quant<Tin, true><<<grid, kFwdThreads, 0, st>>>(x, (int)M, (int)I, (int)ldh, qa, (int)ldqa, sa, qh, (int)ldqh, sh,
+                                                         n_rows, mode);
     else
-        k_swiglu_quant<Tin, false><<<grid, 256, 0, st>>>(x, M, I, ldh, qa, ldqa, sa, qh, ldqh, sh, n_rows, mode);
+        k_swiglu_quant<Tin, false><<<grid, kFwdThreads, 0, st>>>(x, (int)M, (int)I, (int)ldh, qa, (int)ldqa, sa, qh, (int)ldqh, sh,
+                                                          n_rows, mode);
     return cudaGetLastError();
 }
 
@@ -623,7 +626,7 @@ cudaError_t bwd(const BwdParams& p, cudaStream_t st)
     static constexpr int kBytes = (int)sizeof(BwdShared<Tda>);
     const cudaError_t e = allow_smem<k_swiglu_bwd<Tda>>(kBytes);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = (p.M + 127) / 128 * (p.I / 128);
+    const int64_t tiles = ((int64_t)p.M + 127) / 128 * (p.I / 128);
     const int64_t sms = device_sm_count();
     const unsigned grid = (unsigned)(tiles < sms ? tiles : sms);
     k_swiglu_bwd<Tda><<<grid, kBwdThreads, kBytes, st>>>(p);
@@ -651,8 +654,8 @@ cudaError_t launch_swiglu_bwd(const uint8_t* qh, int64_t ldqh, const float* sh, 
     p.qh = qh;
     p.sh = sh;
     p.da = da;
-    p.ldqh = ldqh;
-    p.ldda = ldda;
+    p.ldqh = (int)ldqh;
+    p.ldda = (int)ldda;
     p.dh = static_cast<__nv_bfloat16*>(dh);
     p.qdh = qdh;
     p.sdh = sdh;
@@ -661,12 +664,12 @@ cudaError_t launch_swiglu_bwd(const uint8_t* qh, int64_t ldqh, const float* sh, 
     p.qaT = qaT;
     p.saT = saT;
     p.n_rows = n_rows;
-    p.M = M;
-    p.I = I;
-    p.lddh = lddh;
-    p.ldqdh = ldqdh;
-    p.ldqdhT = ldqdhT;
-    p.ldqaT = ldqaT;
+    p.M = (int)M;
+    p.I = (int)I;
+    p.lddh = (int)lddh;
+    p.ldqdh = (int)ldqdh;
+    p.ldqdhT = (int)ldqdhT;
+    p.ldqaT = (int)ldqaT;
     p.mode = mode;
     p.timeout_ns = wait_timeout_ns();
     return in_dtype == FP8_IN_BF16 ? bwd<__nv_bfloat16>(p, st) : bwd<float>(p, st);
