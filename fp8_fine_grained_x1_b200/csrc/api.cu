@@ -370,7 +370,7 @@ FP8FG_API int fp8_swiglu_quant(const void* h, int in_dtype, int64_t M, int64_t I
     if (!is_in(in_dtype) || !is_mode(scale_mode)) return FP8_ERR_DTYPE;
     if (M < 0 || M > kMaxDim || I <= 0 || I > kMaxDim / 2 || I % 128 || ldh < 2 * I || ldh > kMaxDim ||
         ldqa < I || ldqa > kMaxDim || (qh && (ldqh < 2 * I || ldqh > kMaxDim)) ||
-        (M + 31) / 32 > kMaxDim / (I / 128))
+        (M + 15) / 16 > kMaxDim / (I / 128))
         return FP8_ERR_SHAPE;
     if (M == 0) return FP8_OK;
     if (!h || !qa || !sa || !qh != !sh) return FP8_ERR_NULL;

@@ -96,14 +96,17 @@ __device__ __forceinline__ uint32_t scale_cvt4(F2 a, F2 b, float inv)
 
 // ------------------------------------------------------------ forward
 
-// Threads of a CTA, rows per lane, and CTAs per SM (which caps the registers at 80): of 1 to 4 rows
-// and 64 to 256 threads these ran fastest over the range of sizes (4096 x 9216: 45.3 us, 135168 x 2048:
-// 305; 256 threads 46.8 and 315; 3 rows and 5 CTAs 45.5 and 300, but 3.9 us instead of 2.9 for 7 x 512;
-// others 47 to 54 and 315 to 358).
+// Threads of a CTA, rows per lane, and CTAs per SM (which caps the registers at 80).  BF16: of 1 to 4
+// rows and 64 to 256 threads these ran fastest over the range of sizes (4096 x 9216: 45.3 us, 135168 x
+// 2048: 305; 256 threads 46.8 and 315; 3 rows and 5 CTAs 45.5 and 300, but 3.8 us instead of 3.3 for
+// 1000 x 2048; others 47 to 54 and 315 to 358).  FP32 rows hold twice the registers: 16384 x 2048 takes
+// 57 us with one row, 69 with two, whose loads spill, 58 with two in 4 CTAs.
 constexpr int kFwdThreads = 128;
-constexpr int kFwdSteps = 2;
 constexpr int kFwdCtasPerSm = 6;
-constexpr int kFwdRowsPerCta = kFwdThreads / 8 * kFwdSteps;   // 8 lanes a row
+template <typename T>
+constexpr int kFwdSteps = sizeof(T) == 2 ? 2 : 1;
+template <typename T>
+constexpr int kFwdRowsPerCta = kFwdThreads / 8 * kFwdSteps<T>;      // 8 lanes a row
 
 // Lane l of a row's 8 lanes owns 16 of a group's 128 channels, in 16-byte pieces 128 bytes
 // apart (so that the 8 lanes of a row read 128 contiguous bytes at a time): BF16 2 pieces of 8
@@ -188,13 +191,13 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdCtasPerSm) k_swiglu_quant(
     using V = Sixteen<Tin>;
     const int l = threadIdx.x & 7;
     const uint32_t ncb = (uint32_t)I / 128, rb = blockIdx.x / ncb, cb = blockIdx.x - rb * ncb;
-    const uint32_t m0 = rb * kFwdRowsPerCta + (threadIdx.x >> 3);    // may pass 2^31 by less than a CTA's rows
+    const uint32_t m0 = rb * kFwdRowsPerCta<Tin> + (threadIdx.x >> 3);    // may pass 2^31 by less than a CTA's rows
     const uint32_t rows = (uint32_t)live_rows(n_rows, M);
     const int col = (int)cb * 128 + l * V::kPer;
 
-    V rg[kFwdSteps], ru[kFwdSteps];
+    V rg[kFwdSteps<Tin>], ru[kFwdSteps<Tin>];
 #pragma unroll
-    for (int i = 0; i < kFwdSteps; ++i) {
+    for (int i = 0; i < kFwdSteps<Tin>; ++i) {
         const uint32_t m = m0 + kFwdThreads / 8 * i;
         const Tin* src = h + (int64_t)(int)(m < rows ? m : 0) * ldh + col;
 #pragma unroll
@@ -207,7 +210,7 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdCtasPerSm) k_swiglu_quant(
         }
     }
 #pragma unroll
-    for (int i = 0; i < kFwdSteps; ++i) {
+    for (int i = 0; i < kFwdSteps<Tin>; ++i) {
         const uint32_t m = m0 + kFwdThreads / 8 * i;
         const bool live = m < rows;
         F2 g[8], u[8], a[8];
@@ -609,7 +612,7 @@ template <typename Tin>
 cudaError_t fwd(const void* h, int64_t M, int64_t I, int64_t ldh, uint8_t* qa, int64_t ldqa, float* sa,
                 uint8_t* qh, int64_t ldqh, float* sh, const int32_t* n_rows, int mode, cudaStream_t st)
 {
-    const unsigned grid = (unsigned)((M + kFwdRowsPerCta - 1) / kFwdRowsPerCta * (I / 128));
+    const unsigned grid = (unsigned)((M + kFwdRowsPerCta<Tin> - 1) / kFwdRowsPerCta<Tin> * (I / 128));
     const Tin* x = static_cast<const Tin*>(h);
     if (qh)
         k_swiglu_quant<Tin, true><<<grid, kFwdThreads, 0, st>>>(x, (int)M, (int)I, (int)ldh, qa, (int)ldqa, sa, qh, (int)ldqh, sh,
