@@ -395,7 +395,7 @@ FP8FG_API int fp8_swiglu_bwd(const uint8_t* qh, int64_t ldqh, const float* sh, c
         ldda < I || ldda > kMaxDim || (dh && (lddh < 2 * I || lddh > kMaxDim)) ||
         (qdh && (ldqdh < 2 * I || ldqdh > kMaxDim)) || (qdhT && (ldqdhT < M || ldqdhT > kMaxDim)) ||
         (qaT && (ldqaT < M || ldqaT > kMaxDim)) || ((qdhT || qaT) && M % 128) ||
-        (M + 127) / 128 > kMaxDim / (I / 128))
+        (M + 15) / 16 > kMaxDim / (I / 128))
         return FP8_ERR_SHAPE;
     if (M == 0) return FP8_OK;
     if (!qh || !sh || !da || !qdh != !sdh || !qdhT != !sdhT || !qaT != !saT ||

@@ -94,6 +94,12 @@ __device__ __forceinline__ uint32_t scale_cvt4(F2 a, F2 b, float inv)
     return cvt4(lo(x), hi(x), lo(y), hi(y));
 }
 
+__device__ __forceinline__ uint32_t pack_bf16(F2 v)
+{
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo(v), hi(v));
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+
 // ------------------------------------------------------------ forward
 
 // Threads of a CTA, rows per lane, and CTAs per SM (which caps the registers at 80).  BF16: of 1 to 4
@@ -132,6 +138,21 @@ struct Sixteen<__nv_bfloat16> {
         *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[1]);
         *reinterpret_cast<uint2*>(dst + 64) = make_uint2(c[2], c[3]);
     }
+    static __device__ __forceinline__ void load_codes(const uint8_t* src, uint32_t (&c)[4])
+    {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+                         : "=r"(c[2 * i]), "=r"(c[2 * i + 1])
+                         : "l"(src + 64 * i));
+    }
+    static __device__ __forceinline__ void store_bf16(__nv_bfloat16* dst, const F2 (&v)[8])
+    {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<uint4*>(dst + 64 * i) =
+                make_uint4(pack_bf16(v[4 * i]), pack_bf16(v[4 * i + 1]), pack_bf16(v[4 * i + 2]), pack_bf16(v[4 * i + 3]));
+    }
 };
 template <>
 struct Sixteen<float> {
@@ -149,6 +170,18 @@ struct Sixteen<float> {
     {
 #pragma unroll
         for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(dst + 32 * i) = c[i];
+    }
+    static __device__ __forceinline__ void load_codes(const uint8_t* src, uint32_t (&c)[4])
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(c[i]) : "l"(src + 32 * i));
+    }
+    static __device__ __forceinline__ void store_bf16(__nv_bfloat16* dst, const F2 (&v)[8])
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint2*>(dst + 32 * i) = make_uint2(pack_bf16(v[2 * i]), pack_bf16(v[2 * i + 1]));
     }
 };
 
@@ -263,6 +296,89 @@ constexpr int kBwdThreads = 512;
 constexpr int kBwdWarps = kBwdThreads / 32;     // 16
 constexpr int kBwdTok = 128 / kBwdWarps;        // 8 tokens per warp
 
+// dG, dU and a of a pair of channels.
+__device__ __forceinline__ void gradients(F2 g, F2 u, F2 da, F2& dg, F2& du, F2& a)
+{
+    const F2 one = f2(1.0f, 1.0f);
+    const F2 sig = sigmoid2(g), silu = g * sig;
+    const F2 rest = fma2(sig, f2(-1.0f, -1.0f), one);              // 1 - s
+    dg = da * u * (sig * fma2(g, rest, one));
+    du = da * silu;
+    a = silu * u;
+}
+
+// Backward without transposed outputs: no group spans rows, so the work is split as the forward's (8
+// lanes own a row's channel block).  16384 x 2048, codes of dH alone: 37.5 us, 46.6 by the tiles of
+// k_swiglu_bwd; one row block alone 2.9 and 5.1.
+template <typename Tda>
+__global__ void __launch_bounds__(kFwdThreads, kFwdCtasPerSm) k_swiglu_bwd_rows(const BwdParams p)
+{
+    using V = Sixteen<Tda>;
+    const int l = threadIdx.x & 7;
+    const uint32_t ncb = (uint32_t)p.I / 128, rb = blockIdx.x / ncb, cb = blockIdx.x - rb * ncb;
+    const uint32_t m0 = rb * kFwdRowsPerCta<Tda> + (threadIdx.x >> 3);
+    const uint32_t rows = (uint32_t)live_rows(p.n_rows, p.M);
+    const int col = (int)cb * 128 + l * V::kPer;
+
+    V rd[kFwdSteps<Tda>];
+    uint32_t cg[kFwdSteps<Tda>][4], cu[kFwdSteps<Tda>][4];
+    float sg[kFwdSteps<Tda>], su[kFwdSteps<Tda>];
+#pragma unroll
+    for (int i = 0; i < kFwdSteps<Tda>; ++i) {
+        const uint32_t m = m0 + kFwdThreads / 8 * i;
+        const int64_t r = (int64_t)(int)(m < rows ? m : 0);
+        sg[i] = su[i] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) cg[i][j] = cu[i][j] = 0;
+#pragma unroll
+        for (int j = 0; j < V::kPieces; ++j) rd[i].r[j] = make_uint4(0, 0, 0, 0);
+        if (m < rows) {
+            V::load_codes(p.qh + r * p.ldqh + col, cg[i]);
+            V::load_codes(p.qh + r * p.ldqh + col + p.I, cu[i]);
+            const Tda* da = static_cast<const Tda*>(p.da) + r * p.ldda + col;
+#pragma unroll
+            for (int j = 0; j < V::kPieces; ++j) rd[i].r[j] = ld_stream16(da + 8 * V::kPer * j);
+            sg[i] = __ldg(p.sh + (int64_t)(int)cb * p.M + r);
+            su[i] = __ldg(p.sh + (int64_t)(int)(ncb + cb) * p.M + r);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kFwdSteps<Tda>; ++i) {
+        const uint32_t m = m0 + kFwdThreads / 8 * i;
+        const bool live = m < rows;
+        F2 da[8], dg[8], du[8];
+        rd[i].get(da);
+        const F2 s0 = f2(sg[i], sg[i]), s1 = f2(su[i], su[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float gf[4], uf[4];
+            decode4_e4m3(cg[i][j], gf);
+            decode4_e4m3(cu[i][j], uf);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                F2 a;
+                gradients(f2(gf[2 * k], gf[2 * k + 1]) * s0, f2(uf[2 * k], uf[2 * k + 1]) * s1, da[2 * j + k],
+                          dg[2 * j + k], du[2 * j + k], a);
+            }
+        }
+        if (p.dh && live) {
+            __nv_bfloat16* dst = p.dh + (int64_t)(int)m * p.lddh + col;
+            V::store_bf16(dst, dg);
+            V::store_bf16(dst + p.I, du);
+        }
+        if (!p.qdh) continue;
+        const float mg = row_max(absmax16(dg)), mu = row_max(absmax16(du));
+        const GroupScale gs = group_scale(l == 1 ? mu : mg, p.mode);
+        if (live && l < 2) p.sdh[(int64_t)(int)(l ? ncb + cb : cb) * p.M + m] = gs.s;
+        uint8_t* dst = p.qdh + (int64_t)(int)m * p.ldqdh + col;
+        uint32_t c[4];
+        encode16(dg, __shfl_sync(0xffffffffu, gs.inv, 0, 8), c);
+        if (live) V::store(dst, c);
+        encode16(du, __shfl_sync(0xffffffffu, gs.inv, 1, 8), c);
+        if (live) V::store(dst + p.I, c);
+    }
+}
+
 struct Tile {
     int32_t tb, cb;         // block of 128 tokens, block of 128 channels
 };
@@ -273,6 +389,7 @@ struct __align__(128) BwdStage {
     uint8_t g[128 * 128];                       // checkpoint codes of the gate and the up half
     uint8_t u[128 * 128];
     Tda da[128 * 128];
+    float scale[2][128];                        // the checkpoint's, of both halves
 };
 
 // FP32 gradients leave room for one stage (96 KB) beside the transposed codes, BF16 ones for two.
@@ -291,12 +408,6 @@ struct __align__(128) BwdShared {
     int abort;
 };
 
-__device__ __forceinline__ uint32_t pack_bf16(F2 v)
-{
-    const __nv_bfloat162 b = __floats2bfloat162_rn(lo(v), hi(v));
-    return *reinterpret_cast<const uint32_t*>(&b);
-}
-
 // 16 bytes global -> shared (its 32-bit address), asynchronously; zeros when `live` is false.
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src)
 {
@@ -305,6 +416,10 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src)
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool live)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
 }
 // This thread's arrival on an mbarrier, once its copies so far have landed.
 __device__ __forceinline__ void cp_arrive(uint64_t* bar)
@@ -315,8 +430,8 @@ __device__ __forceinline__ void cp_arrive(uint64_t* bar)
 // Persistent CTAs of 512 threads over tiles of 128 tokens x 128 channels of I (channel
 // block fastest), which arrive by cp.async while the tile before is worked on: into the other of two
 // stages, or, with FP32 gradients, into the only one once its values are in registers.  (Three TMA
-// boxes instead save a tenth of the instructions, yet the kernel took 645 us instead of 534 then for
-// 135168 x 2048.)
+// boxes instead save a tenth of the instructions, yet took 645 us instead of 534, as the kernel was
+// then, for 135168 x 2048.)
 // Warp w owns tokens 8w .. 8w+7, lane l channels 4l .. 4l+3, so a warp holds whole 1x128
 // groups (one warp reduction each; lane j derives the scale of group j of the warp's 16 once)
 // and the 128x1 groups combine the warps' maxima through shared memory.  dG, dU and a stay in
@@ -325,11 +440,11 @@ __device__ __forceinline__ void cp_arrive(uint64_t* bar)
 // lane: two wavefronts per store) and leave as whole 128-byte rows.
 // The 16 warps never stop at a common barrier: each of a tile's three hand-overs (part, inv,
 // outT) is an mbarrier that a warp arrives on, does work that does not need it, and
-// then waits for -- the rows of the tile before go out and the 1x128 groups get their scales
-// between part and inv, the 1x128 groups are encoded between inv and outT.  The order counts:
-// 4096 x 9216 took 74 us (72 since, by 32-bit offsets), 77 with the 1x128 scales behind the channels', 86 with them or the next
-// tile's loads before the tile before's rows, 87 and 93 with half or all of the 1x128 codes before
-// the channels' scales.  (Waits that suspend instead of spinning: 1 % more.)
+// then waits for -- the 1x128 groups get their scales and the rows of the tile before go out
+// between part and inv, the 1x128 groups are encoded between inv and outT.  (4096 x 9216 takes
+// 70.4 us; 71.1 with the 1x128 scales behind the channels', 75.5 with half of the 1x128 codes
+// before them.  Waits that suspend instead of spinning cost 1 % more; the checkpoint's scales
+// loaded into registers a tile ahead, 2 to 20 %, as the compiler lets them be waited for.)
 // Tokens at or beyond the rows in use count as zero in the 128x1 groups.
 template <typename Tda>
 __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p)
@@ -342,7 +457,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
     const int32_t ncb = p.I / 128;
     const int rows = (int)live_rows(p.n_rows, p.M);
     const int32_t ntb = (int32_t)(((uint32_t)rows + 127) / 128);
-    const bool wantH = p.qdhT != nullptr, wantA = p.qaT != nullptr, wantT = wantH || wantA;
+    const bool wantH = p.qdhT != nullptr, wantA = p.qaT != nullptr;      // one of them at least
 
     if (threadIdx.x == 0) {
         mbar_init(&s.full[0], kBwdThreads);
@@ -396,12 +511,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
                 cp16(dst + kD + i * kStep, live ? da + (int64_t)(i * kStepD) * p.ldda : static_cast<const Tda*>(p.da), live);
             }
         }
+        if (threadIdx.x < 256) {
+            const int t = t0 + (threadIdx.x & 127), half = threadIdx.x >> 7;
+            const bool live = t < rows;
+            cp4(smem_u32(&s.stage[st].scale[0][0]) + threadIdx.x * 4,
+                p.sh + (int64_t)(half * ncb + tile.cb) * p.M + (live ? t : 0), live);
+        }
         cp_arrive(&s.full[st]);
-    };
-    // the checkpoint scale of this lane's (half, token): lanes 0-7 the gate's, 8-15 the up half's
-    auto load_scale = [&](Tile tile) -> float {
-        const int t = tile.tb < ntb ? tile.tb * 128 + w * kBwdTok + (lane & 7) : p.M;
-        return lane < 16 && (uint32_t)t < (uint32_t)rows ? __ldg(p.sh + (int64_t)((lane >> 3) * ncb + tile.cb) * p.M + t) : 0.0f;
     };
     // whole 128-byte rows of a tile's transposed codes: 8 threads a row, 64 channels a pass
     auto store_rows = [&](Tile tile) {
@@ -427,7 +543,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
     const int32_t step_tb = (int32_t)gridDim.x / ncb, step_cb = (int32_t)gridDim.x % ncb;
     Tile tile{(int32_t)blockIdx.x / ncb, (int32_t)blockIdx.x % ncb}, prev = tile, next = tile;
     if (tile.tb < ntb) load(tile, 0);
-    float scale = load_scale(tile);
     int it = 0;
     for (; tile.tb < ntb; ++it, prev = tile, tile = next) {
         const int st = NST == 2 ? it & 1 : 0;
@@ -440,7 +555,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
         // two stages: all warps have read the other one, for this one has waited for the
         // previous tile's bPart
         if (NST == 2 && next.tb < ntb) load(next, st ^ 1);
-        const float scale_next = load_scale(next);
         wait(&s.full[st], NST == 2 ? it >> 1 : it);
 
         const int col = tile.cb * 128 + 4 * lane;
@@ -449,10 +563,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
         F2 v[3][kBwdTok][2];      // dG, dU, a
         {
             const BwdStage<Tda>& d = s.stage[st];
+            float sc[2][kBwdTok];
+#pragma unroll
+            for (int i = 0; i < 2 * kBwdTok; i += 4)
+                *reinterpret_cast<float4*>(&sc[0][0] + i) =
+                    *reinterpret_cast<const float4*>(&d.scale[i / kBwdTok][w * kBwdTok + i % kBwdTok]);
 #pragma unroll
             for (int i = 0; i < kBwdTok; ++i) {
                 const int r = w * kBwdTok + i;
-                const float s0 = __shfl_sync(0xffffffffu, scale, i), s1 = __shfl_sync(0xffffffffu, scale, 8 + i);
+                const float s0 = sc[0][i], s1 = sc[1][i];
                 float gf[4], uf[4];
                 decode4_e4m3(*reinterpret_cast<const uint32_t*>(d.g + r * 128 + 4 * lane), gf);
                 decode4_e4m3(*reinterpret_cast<const uint32_t*>(d.u + r * 128 + 4 * lane), uf);
@@ -463,18 +582,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
                 const F2 sg = f2(s0, s0), su = f2(s1, s1);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const F2 g = f2(gf[2 * k], gf[2 * k + 1]) * sg;
-                    const F2 u = f2(uf[2 * k], uf[2 * k + 1]) * su;
-                    const F2 one = f2(1.0f, 1.0f);
-                    const F2 sig = sigmoid2(g), silu = g * sig;
-                    const F2 rest = fma2(sig, f2(-1.0f, -1.0f), one);              // 1 - s
-                    v[0][i][k] = da[k] * u * (sig * fma2(g, rest, one));
-                    v[1][i][k] = da[k] * silu;
-                    v[2][i][k] = silu * u;
+                    gradients(f2(gf[2 * k], gf[2 * k + 1]) * sg, f2(uf[2 * k], uf[2 * k + 1]) * su, da[k], v[0][i][k],
+                              v[1][i][k], v[2][i][k]);
                 }
             }
         }
-        scale = scale_next;
 
         // per-warp column maxima for the 128x1 groups
 #pragma unroll
@@ -491,11 +603,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
             *reinterpret_cast<float4*>(&s.part[x][w][4 * lane]) = make_float4(a[0], a[1], a[2], a[3]);
         }
         arrive(&s.bPart);
-        if (wantT && it > 0) {
-            wait(&s.bOut, it - 1);
-            store_rows(prev);
-        }
-        // maxima and scales of the 1x128 groups (lane j: group j of the warp's 16), while others get here
+        // maxima and scales of the 1x128 groups (lane j: group j of the warp's 16)
         GroupScale gs{};
         if (p.qdh) {
 #pragma unroll
@@ -510,26 +618,28 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
             gs = group_scale(s.rmax[w][lane & 15], p.mode);
             __syncwarp();
         }
+        if (it > 0) {
+            wait(&s.bOut, it - 1);
+            store_rows(prev);
+        }
         wait(&s.bPart, it);
         if (NST == 1 && next.tb < ntb) load(next, 0);
-        if (wantT) {
-            // channel scales; a warp past the 384 channels arrives all the same: bInv also
-            // says that every warp has stored the previous tile's rows
-            if (threadIdx.x < 384 && (threadIdx.x < 256 ? wantH : wantA)) {
-                const int x = threadIdx.x >> 7, c = threadIdx.x & 127;
-                float a = s.part[x][0][c];
+        // channel scales; a warp past the 384 channels arrives all the same: bInv also
+        // says that every warp has stored the previous tile's rows
+        if (threadIdx.x < 384 && (threadIdx.x < 256 ? wantH : wantA)) {
+            const int x = threadIdx.x >> 7, c = threadIdx.x & 127;
+            float a = s.part[x][0][c];
 #pragma unroll
-                for (int k = 1; k < kBwdWarps - 1; k += 2) a = absmax3(a, s.part[x][k][c], s.part[x][k + 1][c]);
-                const GroupScale gs = group_scale(fmaxf(a, s.part[x][kBwdWarps - 1][c]), p.mode);
-                s.inv[threadIdx.x] = gs.inv;
-                const int ch = tile.cb * 128 + c;
-                if (x < 2)
-                    p.sdhT[(int64_t)tile.tb * (2 * p.I) + x * p.I + ch] = gs.s;
-                else
-                    p.saT[(int64_t)tile.tb * p.I + ch] = gs.s;
-            }
-            arrive(&s.bInv);
+            for (int k = 1; k < kBwdWarps - 1; k += 2) a = absmax3(a, s.part[x][k][c], s.part[x][k + 1][c]);
+            const GroupScale gs = group_scale(fmaxf(a, s.part[x][kBwdWarps - 1][c]), p.mode);
+            s.inv[threadIdx.x] = gs.inv;
+            const int ch = tile.cb * 128 + c;
+            if (x < 2)
+                p.sdhT[(int64_t)tile.tb * (2 * p.I) + x * p.I + ch] = gs.s;
+            else
+                p.saT[(int64_t)tile.tb * p.I + ch] = gs.s;
         }
+        arrive(&s.bInv);
 
         // 1x128 groups and BF16 rows
         if (p.dh) {
@@ -555,8 +665,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
                         *reinterpret_cast<uint32_t*>(dst + x * p.I) = scale_cvt4(v[x][i][0], v[x][i][1], inv);
                 }
         }
-        if (!wantT) continue;
-
         wait(&s.bInv, it);
         const int half = (w & 1) ^ ((lane >> 3) & 1);
 #pragma unroll
@@ -581,7 +689,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
         // part is written again only behind this tile's bInv, inv only behind the next tile's
         // bPart, which a warp arrives on after the reads of inv above.
     }
-    if (wantT && it > 0) {
+    if (it > 0) {
         wait(&s.bOut, it - 1);
         store_rows(prev);
     }
@@ -626,6 +734,11 @@ cudaError_t fwd(const void* h, int64_t M, int64_t I, int64_t ldh, uint8_t* qa, i
 template <typename Tda>
 cudaError_t bwd(const BwdParams& p, cudaStream_t st)
 {
+    if (!p.qdhT && !p.qaT) {
+        const int64_t blocks = ((int64_t)p.M + kFwdRowsPerCta<Tda> - 1) / kFwdRowsPerCta<Tda> * (p.I / 128);
+        k_swiglu_bwd_rows<Tda><<<(unsigned)blocks, kFwdThreads, 0, st>>>(p);
+        return cudaGetLastError();
+    }
     static constexpr int kBytes = (int)sizeof(BwdShared<Tda>);
     const cudaError_t e = allow_smem<k_swiglu_bwd<Tda>>(kBytes);
     if (e != cudaSuccess) return e;
