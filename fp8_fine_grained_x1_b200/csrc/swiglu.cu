@@ -308,10 +308,12 @@ __device__ __forceinline__ void gradients(F2 g, F2 u, F2 da, F2& dg, F2& du, F2&
 }
 
 // Backward without transposed outputs: no group spans rows, so the work is split as the forward's (8
-// lanes own a row's channel block).  16384 x 2048, codes of dH alone: 37.5 us, 46.6 by the tiles of
-// k_swiglu_bwd; one row block alone 2.9 and 5.1.
+// lanes own a row's channel block).  16384 x 2048, codes of dH alone: 35.7 us (FP32 dA 43.9), 46.6
+// (60.5) by the tiles of k_swiglu_bwd; 128 x 512 3.0 and 5.1.  Swept as the forward: 6 CTAs per SM 37.9
+// (49.0), 10 of one row 39.4 (44.6), 4 of three 41.3.
+constexpr int kBwdRowsCtasPerSm = 8;
 template <typename Tda>
-__global__ void __launch_bounds__(kFwdThreads, kFwdCtasPerSm) k_swiglu_bwd_rows(const BwdParams p)
+__global__ void __launch_bounds__(kFwdThreads, kBwdRowsCtasPerSm) k_swiglu_bwd_rows(const BwdParams p)
 {
     using V = Sixteen<Tda>;
     const int l = threadIdx.x & 7;
