@@ -273,6 +273,33 @@ def test_what_is_not_finite_stays_in_its_groups(bad):
     assert fg.fp8_get_status() == fg.FP8_OK
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("M", [1, 31, 200])
+def test_backward_by_rows_in_use_and_strided(M, dtype):
+    """Without outputs along tokens: the bits of the full call's rows, rows behind those in use neither read
+    nor written, outputs in slices of wider buffers."""
+    I = 384
+    q, s, h = _checkpoint(256, I, 17)
+    da, dv = _input(_da(256, I, 11), dtype, pad=8)
+    full = fg.swiglu_bwd(to_dev(q), to_dev(s), da, ("dh", "qdh", "qaT"))
+    q, s = to_dev(q)[:M].contiguous(), to_dev(s)[:, :M].contiguous()
+    for n in (None, 0, 1, M - 1, M, M + 5, -3):
+        want = M if n is None else min(max(n, 0), M)
+        dh, qdh = _junk((M, 2 * I + 16), torch.bfloat16), _junk((M, 2 * I + 32), torch.uint8)
+        sdh = _junk((2 * I // 128, M), torch.float32)
+        bad, qb, sb = da[:M].clone(), q.clone(), s.clone()
+        bad[want:], qb[want:], sb[:, want:] = float("nan"), 0x7F, float("nan")
+        fg.fp8_swiglu_bwd(qb, sb, bad, dh=dh[:, :2 * I], qdh=qdh[:, :2 * I], sdh=sdh,
+                          n_rows=None if n is None else torch.tensor([n], dtype=torch.int32, device=dev()))
+        assert torch.equal(dh[:want, :2 * I], full["dh"][:want]) and torch.equal(qdh[:want, :2 * I], full["qdh"][:want])
+        assert torch.equal(sdh[:, :want], full["sdh"][:, :want])
+        assert _untouched(dh[want:]) and _untouched(dh[:, 2 * I:]) and _untouched(qdh[want:])
+        assert _untouched(qdh[:, 2 * I:]) and _untouched(sdh[:, want:])
+    grad, mag = mlp.swiglu_grads(h, dv)
+    _check_rows(_np(full["qdh"]), _np(full["sdh"]), grad, ERR * mag, fg.SCALE_FP32)
+    assert fg.fp8_get_status() == fg.FP8_OK
+
+
 def test_strided_outputs():
     """Codes written into slices of wider buffers, the rest of them untouched."""
     M, I = 128, 256
@@ -358,3 +385,26 @@ def test_offsets_beyond_32_bits():
     out = fg.swiglu_bwd(qh, sh, da, ("qdh",))
     refb = fg.swiglu_bwd(ref[2], ref[3], dt, ("qdh",))
     assert torch.equal(out["qdh"][-300:], refb["qdh"]) and torch.equal(out["sdh"][:, -300:], refb["sdh"])
+
+
+def test_transposed_offsets_beyond_32_bits():
+    """The last token blocks of tensors of more than 2^32 elements give the bits that they give alone."""
+    I = 2048
+    M = 2 ** 32 // (2 * I) + 256
+    d = dev()
+    q, s, _ = _checkpoint(256, I, 23)
+    qh = torch.zeros((M, 2 * I), dtype=torch.uint8, device=d)
+    sh = torch.ones((2 * I // 128, M), dtype=torch.float32, device=d)
+    da = torch.zeros((M, I), dtype=torch.bfloat16, device=d)
+    qh[-256:], sh[:, -256:] = to_dev(q), to_dev(s)
+    tail = _input(_da(256, I, 12), "bf16")[0]
+    da[-256:] = tail
+    outputs = ("dh", "qdh", "qdhT", "qaT")
+    got, ref = fg.swiglu_bwd(qh, sh, da, outputs), fg.swiglu_bwd(to_dev(q), to_dev(s), tail.contiguous(), outputs)
+    for name in ("dh", "qdh"):
+        assert torch.equal(got[name][-256:], ref[name]), name
+    for name in ("sdh", "qdhT", "qaT"):
+        assert torch.equal(got[name][:, -256:], ref[name]), name
+    for name in ("sdhT", "saT"):
+        assert torch.equal(got[name][-2:], ref[name]), name
+    assert fg.fp8_get_status() == fg.FP8_OK
