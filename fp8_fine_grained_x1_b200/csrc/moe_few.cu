@@ -391,6 +391,7 @@ __device__ __forceinline__ void tma_prefetch_l2(const CUtensorMap* map, int32_t 
 
 // A CTA lets the next kernel start when this many of its units are left to load.
 constexpr uint32_t TRIGGER_UNITS = 4;
+// Units of its successor's that it fetches into L2 at its end (4 to 12 measure the same; 24 cost 3 us).
 constexpr int PREFETCH_UNITS = 8;
 
 // Run by the whole of a warp: lane 0 arms the stage barrier and issues its TMA and bulk copies,
