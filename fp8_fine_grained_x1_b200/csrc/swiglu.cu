@@ -445,7 +445,7 @@ __device__ __forceinline__ void cp_arrive(uint64_t* bar)
 // then waits for -- the 1x128 groups get their scales and the rows of the tile before go out
 // between part and inv, the 1x128 groups are encoded between inv and outT.  (4096 x 9216 takes
 // 70.4 us; 71.1 with the 1x128 scales behind the channels', 75.5 with half of the 1x128 codes
-// before them.  Waits that suspend instead of spinning cost 1 % more; the checkpoint's scales
+// before them.  Waits that suspend instead of spinning cost 2 % more; the checkpoint's scales
 // loaded into registers a tile ahead, 2 to 20 %, as the compiler lets them be waited for.)
 // Tokens at or beyond the rows in use count as zero in the 128x1 groups.
 template <typename Tda>
