@@ -69,6 +69,11 @@ constexpr int SLOTS = 8;                        // scale slots (at least MAX_STA
 constexpr int MAX_STAGES = 6;
 // A CTA takes at least this many units (or a whole tile): fewer would only leave more parts to add.
 constexpr uint32_t MIN_UNITS = 2;
+// And no more CTAs than this share a tile on average, or the kernels behind are busy adding its parts: up
+// to 32 tokens (27 tokens, 34 experts of 512 x 1664 x 384: 41 us; 48 with 16 parts, 63 with 8), and more
+// (87 tokens, 10 of 4096 x 128 x 6272: 36 us; 47 with 16 parts, 68 tokens, 24 of 1024 x 640 x 768: 36;
+// 64 without a limit).
+constexpr uint32_t MAX_PARTS = 32, MAX_PARTS_ROWS = 8;
 // Ring bytes: up to 16 tokens leave room for a CTA of each phase on an SM (phase 2's first weights
 // then load while phase 1 drains); more tokens get one CTA with a deeper ring.
 __host__ __device__ constexpr uint32_t ring_budget(int nb) { return (nb <= 16 ? 104 : 216) * 1024; }
@@ -328,7 +333,7 @@ __device__ __forceinline__ Range few_range(const Few& f, int n_act, uint32_t cta
     r.per = PHASE == 1 ? (uint32_t)(f.K / BK) : n_act * J;
     r.U = (PHASE == 1 ? n_act * J : (n_act ? (uint32_t)((f.N + 255) / 256) : 0)) * r.per;
     const uint32_t tiles = r.per ? r.U / r.per : 0, want = r.U / MIN_UNITS > tiles ? r.U / MIN_UNITS : tiles;
-    r.P = want < ctas ? want : ctas;
+    r.P = min(min(want, ctas), tiles * (f.Tp > MAX_COLUMN_TOKENS ? MAX_PARTS_ROWS : MAX_PARTS));
     r.u0 = blockIdx.x < r.P ? r.begin(blockIdx.x) : 0;
     r.u1 = blockIdx.x < r.P ? r.begin(blockIdx.x + 1) : 0;
     return r;
@@ -518,12 +523,9 @@ __device__ void few_mma(const Few& f, const Range& r, uint8_t* smem, FewShared<N
     mbar_wait_drain(&sh.drain, 0, f.timeout_ns);
 }
 
-// Where channel c of token t lies in a row block's T x 128 sums: as the promotion's threads, one a
-// channel or one a token, can write them whole lines at a time.
-__device__ __forceinline__ int sum_at(const Few& f, int c) { return f.Tp > MAX_COLUMN_TOKENS ? (c >> 2) * f.T * 4 + (c & 3) : c; }
-__device__ __forceinline__ int sum_step(const Few& f) { return f.Tp > MAX_COLUMN_TOKENS ? 4 : 128; }      // to the next token
-
-// The parts of a tile: CTAs c0..c1 hold one each, in slots of `stride` floats, see sum_at.
+// The parts of a tile: CTAs c0..c1 hold one each, in slots of `stride` floats: two row
+// blocks of [T][128], or, with tokens as rows, [128 / 4][T][4], as the promotion's threads can write whole
+// lines.
 struct Parts {
     const float* part;
     Range r;
@@ -810,8 +812,8 @@ __global__ void __launch_bounds__(num_threads(NB), NB <= 16 ? 2 : 1)
                      : "memory");
 }
 
-// Up to 32 tokens.  Block = tile of phase 1: adds its parts for the tokens routed to its expert, 8 at
-// a time, thread = channel; SwiGLU and 1x128 quantization.  Tokens not routed here (gate weight 0)
+// Up to 32 tokens.  Block = (tile of phase 1, every gridDim.y-th 8 tokens): adds its parts for the tokens routed to its expert,
+// thread = channel; SwiGLU and 1x128 quantization.  Tokens not routed here (gate weight 0)
 // get zero rows of scale 0.  Everything but the parts is known (k_few_prep had completed before phase 1
 // let this kernel start), and done, before phase 1 ends.
 constexpr int ACT_TOKENS = 8;
@@ -834,7 +836,7 @@ __global__ void __launch_bounds__(128) k_few_act(const Few f, uint32_t ctas)
     const Range r = few_range<1>(f, live ? n_act : 1, ctas);
     const Parts p(f, r, (live ? tile : 0) * r.per);
     __syncthreads();
-    if (!live) {
+    if (!live || (blockIdx.y > 0 && (int)blockIdx.y * ACT_TOKENS >= n)) {
         wait_previous();
         return;
     }
@@ -848,10 +850,10 @@ __global__ void __launch_bounds__(128) k_few_act(const Few f, uint32_t ctas)
     int round = -1;
     asm volatile("" : "+r"(round));
 #pragma unroll 1
-    for (; round * ACT_TOKENS < n; ++round) {
+    for (; round * ACT_TOKENS < n; round += round < 0 ? 1 + (int)blockIdx.y : (int)gridDim.y) {
         const bool real = round >= 0;
         const int c = real ? round * ACT_TOKENS : 0;
-        if (round == 0) wait_previous();
+        if (round == (int)blockIdx.y) wait_previous();
         float g[ACT_TOKENS], u[ACT_TOKENS];
 #pragma unroll
         for (int i = 0; i < ACT_TOKENS; ++i) g[i] = u[i] = 0.0f;
@@ -902,11 +904,11 @@ __global__ void __launch_bounds__(128) k_few_act(const Few f, uint32_t ctas)
         // (the next round's writes of codes follow a barrier that these reads precede)
     }
     if (n == 0) wait_previous();
-    if (tid < 32 && lane < f.T && gw == 0.0f) as[lane] = 0.0f;
+    if (blockIdx.y == 0 && tid < 32 && lane < f.T && gw == 0.0f) as[lane] = 0.0f;
 }
 
 // The same behind few_promotion_rows, whose sums lie [channel / 4][token][4]: block = (tile of phase 1,
-// every second 32 of the tokens routed to its expert), thread = token and 32 channels, so that all lanes work and a
+// every gridDim.y-th 32 of the tokens routed to its expert), thread = token and 32 channels, so that all lanes work and a
 // token's 64 values need no shuffle.  Codes of tokens not routed here are left as they are: phase 2 does
 // not add what it makes of them.
 __global__ void __launch_bounds__(128) k_few_act_rows(const Few f, uint32_t ctas)
@@ -999,8 +1001,7 @@ __global__ void __launch_bounds__(256) k_few_out(const Few f, uint32_t ctas)
     const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const Range r = few_range<2>(f, n_act ? n_act : 1, ctas);
     const Parts p(f, r, blockIdx.x * r.per);
-    const int step = sum_step(f);
-    const int64_t at = (int64_t)blk * f.T * 128 + t0 * step + sum_at(f, row);
+    const int64_t at = (int64_t)blk * f.T * 128 + (int64_t)t0 * 128 + row;
     wait_previous();
     if (n >= f.N || (n_act && p.c0 == p.c1)) return;
     float v[OUT_TOKENS];
@@ -1014,7 +1015,7 @@ __global__ void __launch_bounds__(256) k_few_out(const Few f, uint32_t ctas)
             for (int q = 0; q < OUT_PARTS; ++q) {
                 const float* src = p.at(c + q <= p.c1 ? c + q : p.c1) + at;
 #pragma unroll
-                for (int i = 0; i < OUT_TOKENS; ++i) x[q][i] = __ldcg(src + (t0 + i < f.T ? i * step : 0));
+                for (int i = 0; i < OUT_TOKENS; ++i) x[q][i] = __ldcg(src + (t0 + i < f.T ? i * 128 : 0));
             }
 #pragma unroll
             for (int q = 0; q < OUT_PARTS; ++q)
@@ -1025,6 +1026,45 @@ __global__ void __launch_bounds__(256) k_few_out(const Few f, uint32_t ctas)
 #pragma unroll
     for (int i = 0; i < OUT_TOKENS; ++i)
         if (t0 + i < f.T) store_out(f, t0 + i, n, v[i]);
+}
+
+// The same behind few_promotion_rows: block = (64 columns, 32 tokens), warp = 8 adjacent columns, thread = one
+// token's 8.
+constexpr int OUT_ROWS_PARTS = 4;
+
+__global__ void __launch_bounds__(256) k_few_out_rows(const Few f, uint32_t ctas)
+{
+    const int n_act = __ldcg(f.n_act), lane = threadIdx.x & 31, t = 32 * blockIdx.y + lane;
+    const uint32_t tile = blockIdx.x >> 2;
+    const int col = (int)(blockIdx.x & 3) * 64 + (int)(threadIdx.x >> 5) * 8;         // of the tile
+    const int64_t n = (int64_t)tile * 256 + col;
+    const Range r = few_range<2>(f, n_act ? n_act : 1, ctas);
+    const Parts p(f, r, tile * r.per);
+    const int at = (col >> 7) * f.T * 128 + (col & 127) * f.T + (t < f.T ? t : 0) * 4;
+    wait_previous();
+    if (n >= f.N || t >= f.T || (n_act && p.c0 == p.c1)) return;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    if (n_act) {
+#pragma unroll 1
+        for (uint32_t c = p.c0; c <= p.c1; c += OUT_ROWS_PARTS) {
+            float4 x[OUT_ROWS_PARTS][2];
+#pragma unroll
+            for (int q = 0; q < OUT_ROWS_PARTS; ++q) {
+                const float* src = p.at(c + q <= p.c1 ? c + q : p.c1) + at;
+                x[q][0] = __ldcg(reinterpret_cast<const float4*>(src));
+                x[q][1] = __ldcg(reinterpret_cast<const float4*>(src + 4 * f.T));
+            }
+#pragma unroll
+            for (int q = 0; q < OUT_ROWS_PARTS; ++q) {
+                if (c + q > p.c1) break;
+                v[0] += x[q][0].x, v[1] += x[q][0].y, v[2] += x[q][0].z, v[3] += x[q][0].w;
+                v[4] += x[q][1].x, v[5] += x[q][1].y, v[6] += x[q][1].z, v[7] += x[q][1].w;
+            }
+        }
+    }
+    store_out8(f, t, n, v);
 }
 
 // ------------------------------------------------------------ host side
@@ -1065,16 +1105,23 @@ int launch_few_gemms(const Few& f, const CUtensorMap& tmW13, const CUtensorMap& 
     if (cudaLaunchKernelEx(&cfg, k_few_gemm<1, NB>, tmW13, tmX, tmW2, f) != cudaSuccess) return FP8_ERR_LAUNCH;
     const int64_t A = (int64_t)f.T * f.k < f.G ? (int64_t)f.T * f.k : f.G;
     cudaLaunchConfig_t act = cfg;
-    act.gridDim = dim3((unsigned)(A * (f.I / 128)), token_rows(NB) ? 2u : 1u, 1);
+    // the tokens of a tile in several blocks where there are few tiles
+    const unsigned tiles = (unsigned)(A * (f.I / 128)), spread = (2 * ctas + tiles - 1) / tiles;
+    const unsigned most = token_rows(NB) ? 4 : (unsigned)(f.T + ACT_TOKENS - 1) / ACT_TOKENS;
+    act.gridDim = dim3(tiles, max(token_rows(NB) ? 2u : 1u, min(spread, most)), 1);
     act.blockDim = dim3(128, 1, 1);
     act.dynamicSmemBytes = 0;
     if (cudaLaunchKernelEx(&act, token_rows(NB) ? k_few_act_rows : k_few_act, f, (uint32_t)ctas) != cudaSuccess)
         return FP8_ERR_LAUNCH;
     if (cudaLaunchKernelEx(&cfg, k_few_gemm<2, NB>, tmW2, tmA, tmW2, f) != cudaSuccess) return FP8_ERR_LAUNCH;
-    cfg.gridDim = dim3((unsigned)((f.N + 255) / 256), (unsigned)((f.T + OUT_TOKENS - 1) / OUT_TOKENS), 1);
+    const unsigned tiles2 = (unsigned)((f.N + 255) / 256);
+    cfg.gridDim = token_rows(NB) ? dim3(4 * tiles2, (unsigned)((f.T + 31) / 32), 1)
+                                 : dim3(tiles2, (unsigned)((f.T + OUT_TOKENS - 1) / OUT_TOKENS), 1);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, k_few_out, f, (uint32_t)ctas) == cudaSuccess ? FP8_OK : FP8_ERR_LAUNCH;
+    return cudaLaunchKernelEx(&cfg, token_rows(NB) ? k_few_out_rows : k_few_out, f, (uint32_t)ctas) == cudaSuccess
+               ? FP8_OK
+               : FP8_ERR_LAUNCH;
 }
 
 }  // namespace

@@ -199,6 +199,17 @@ def test_a_bad_expert_spoils_only_its_tokens(T):
     assert fg.fp8_get_status() == fg.FP8_OK
 
 
+@pytest.mark.parametrize("T,k,G,K,I,N", [(1, 1, 3, 4096, 128, 128), (30, 3, 4, 2048, 128, 256),
+                                         (32, 4, 5, 256, 2048, 128), (87, 1, 4, 2048, 128, 1152),
+                                         (128, 2, 3, 256, 2048, 128)])
+def test_few_tiles_in_many_parts(T, k, G, K, I, N):
+    """Long products of few tiles, whose parts many CTAs hold; all tokens of an expert in one tile."""
+    case = _case(T, k, G, K, I, N, seed=T + K)
+    got = _run(case)
+    _check(got, case)
+    assert torch.equal(got, _run(case)) and fg.fp8_get_status() == fg.FP8_OK
+
+
 @pytest.mark.parametrize("T,out", [(3, torch.bfloat16), (40, torch.float32), (128, torch.bfloat16)])
 def test_many_output_columns(T, out):
     """More output tiles than CTAs: whole tiles are rounded and stored by the CTA that added them up."""
