@@ -406,7 +406,7 @@ class MoeMlpStep:
     dispatched to 128-padded groups, and the SwiGLU between the two grouped GEMMs
     quantizes the rows in use for the second; H is BF16 there and FP32 in the
     few-token form.  On 32 experts of 7168 x 2048, top-8, the few-token form took
-    70, 196, 240, 249 and 275 us for 1, 8, 32, 64 and 128 tokens, the dispatched
+    70, 196, 240, 249 and 272 us for 1, 8, 32, 64 and 128 tokens, the dispatched
     form 177, 389, 461, 496 and 512: it is taken wherever it can be.  `few`
     overrides the choice."""
 
