@@ -23,6 +23,7 @@ output tensors with torch first.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -505,39 +506,68 @@ def fp8_device_supported() -> bool:
 
 # ---------------------------------------------------------------- allocating helpers
 
+# With a `stream`, what these allocate belongs to it: the allocator then orders a block's next use behind
+# this one, be it a scratch block freed on return or an output whose memory was in use before.
+
+def _allocating(stream):
+    """Allocations inside are `stream`'s (None: those of torch's current stream)."""
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _handed_out(stream, *outputs):
+    """Outputs allocated on `stream`, for a caller on another: once freed, their memory is not used
+    again before the caller's stream is done with them."""
+    import torch
+    if stream is not None and outputs:
+        caller = torch.cuda.current_stream(outputs[0].device)
+        if caller != stream:
+            for t in outputs:
+                if t is not None:
+                    t.record_stream(caller)
+
+
 def quant_act_1x128(x, scale_mode: int = SCALE_FP32, stream=None):
     import torch
     M, K = x.shape
-    q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
-    s = torch.empty((K // 128, M), dtype=torch.float32, device=x.device)
+    with _allocating(stream):
+        q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        s = torch.empty((K // 128, M), dtype=torch.float32, device=x.device)
     fp8_quant_act_1x128(x, q, s, scale_mode, stream)
+    _handed_out(stream, q, s)
     return q, s
 
 
 def quant_act_128x1(x, scale_mode: int = SCALE_FP32, stream=None):
     import torch
     T, C = x.shape
-    q = torch.empty((C, T), dtype=torch.uint8, device=x.device)
-    s = torch.empty((T // 128, C), dtype=torch.float32, device=x.device)
+    with _allocating(stream):
+        q = torch.empty((C, T), dtype=torch.uint8, device=x.device)
+        s = torch.empty((T // 128, C), dtype=torch.float32, device=x.device)
     fp8_quant_act_128x1(x, q, s, scale_mode, stream)
+    _handed_out(stream, q, s)
     return q, s
 
 
 def requant_1x128_to_128x1(q, sA, scale_mode: int = SCALE_FP32, stream=None):
     import torch
     T, C = q.shape
-    qT = torch.empty((C, T), dtype=torch.uint8, device=q.device)
-    s = torch.empty((T // 128, C), dtype=torch.float32, device=q.device)
+    with _allocating(stream):
+        qT = torch.empty((C, T), dtype=torch.uint8, device=q.device)
+        s = torch.empty((T // 128, C), dtype=torch.float32, device=q.device)
     fp8_requant_1x128_to_128x1(q, sA, qT, s, scale_mode, stream)
+    _handed_out(stream, qT, s)
     return qT, s
 
 
 def quant_w_128x128(w, scale_mode: int = SCALE_FP32, stream=None):
     import torch
     N, K = w.shape
-    q = torch.empty((N, K), dtype=torch.uint8, device=w.device)
-    s = torch.empty((N // 128, K // 128), dtype=torch.float32, device=w.device)
+    with _allocating(stream):
+        q = torch.empty((N, K), dtype=torch.uint8, device=w.device)
+        s = torch.empty((N // 128, K // 128), dtype=torch.float32, device=w.device)
     fp8_quant_w_128x128(w, q, s, scale_mode, stream)
+    _handed_out(stream, q, s)
     return q, s
 
 
@@ -546,8 +576,10 @@ def gemm(A, sA, B, sB, out_dtype=None, b_major: int = B_KMAJOR, sb_gran: int = 1
     import torch
     M, K = A.shape
     N = B.shape[0] if b_major == B_KMAJOR else B.shape[1]
-    D = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=A.device)
+    with _allocating(stream):
+        D = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=A.device)
     fp8_blockscaled_gemm(A, sA, B, sB, D, b_major, sb_gran, stream)
+    _handed_out(stream, D)
     return D
 
 
@@ -563,22 +595,26 @@ def moe_dispatch(q, sA, topk, G: int, M_cap: int = None, stream=None):
     k = topk.shape[1]
     M_cap = moe_capacity(T, k, G) if M_cap is None else M_cap
     d = q.device
-    out = dict(q=torch.empty((M_cap, K), dtype=torch.uint8, device=d),
-               sA=torch.empty((K // 128, M_cap), dtype=torch.float32, device=d),
-               offsets=torch.empty(G + 1, dtype=torch.int32, device=d),
-               token_row=torch.empty((T, k), dtype=torch.int32, device=d),
-               row_token=torch.empty(M_cap, dtype=torch.int32, device=d))
-    ws = torch.empty(max(1, fp8_moe_dispatch_workspace_bytes(T, k, G) // 4), dtype=torch.int32,
-                     device=d)
+    with _allocating(stream):
+        out = dict(q=torch.empty((M_cap, K), dtype=torch.uint8, device=d),
+                   sA=torch.empty((K // 128, M_cap), dtype=torch.float32, device=d),
+                   offsets=torch.empty(G + 1, dtype=torch.int32, device=d),
+                   token_row=torch.empty((T, k), dtype=torch.int32, device=d),
+                   row_token=torch.empty(M_cap, dtype=torch.int32, device=d))
+        ws = torch.empty(max(1, fp8_moe_dispatch_workspace_bytes(T, k, G) // 4), dtype=torch.int32,
+                         device=d)
     fp8_moe_dispatch(q, sA, topk, G, out["q"], out["sA"], out["offsets"], out["token_row"],
                      out["row_token"], ws, stream)
+    _handed_out(stream, *out.values())
     return out
 
 
 def grouped_gemm(A, sA, B, sB, group_offsets, out_dtype=None, stream=None):
     import torch
-    D = torch.empty((A.shape[0], B.shape[1]), dtype=out_dtype or torch.bfloat16, device=A.device)
+    with _allocating(stream):
+        D = torch.empty((A.shape[0], B.shape[1]), dtype=out_dtype or torch.bfloat16, device=A.device)
     fp8_grouped_gemm(A, sA, B, sB, group_offsets, D, stream)
+    _handed_out(stream, D)
     return D
 
 
@@ -588,10 +624,12 @@ def swiglu_quant(h, keep: bool = True, scale_mode: int = SCALE_FP32, stream=None
     M, C = h.shape
     u8 = dict(dtype=torch.uint8, device=h.device)
     f32 = dict(dtype=torch.float32, device=h.device)
-    qa, sa = torch.empty((M, C // 2), **u8), torch.empty((C // 256, M), **f32)
-    qh, sh = ((torch.empty((M, C), **u8), torch.empty((C // 128, M), **f32)) if keep
-              else (None, None))
+    with _allocating(stream):
+        qa, sa = torch.empty((M, C // 2), **u8), torch.empty((C // 256, M), **f32)
+        qh, sh = ((torch.empty((M, C), **u8), torch.empty((C // 128, M), **f32)) if keep
+                  else (None, None))
     fp8_swiglu_quant(h, qa, sa, qh, sh, None, scale_mode, stream)
+    _handed_out(stream, qa, sa, qh, sh)
     return qa, sa, qh, sh
 
 
@@ -603,15 +641,17 @@ def swiglu_bwd(qh, sh, da, want=("qdh", "qdhT", "qaT"), scale_mode: int = SCALE_
     u8 = dict(dtype=torch.uint8, device=qh.device)
     f32 = dict(dtype=torch.float32, device=qh.device)
     out = {}
-    if "dh" in want:
-        out["dh"] = torch.empty((M, C), dtype=torch.bfloat16, device=qh.device)
-    if "qdh" in want:
-        out.update(qdh=torch.empty((M, C), **u8), sdh=torch.empty((C // 128, M), **f32))
-    if "qdhT" in want:
-        out.update(qdhT=torch.empty((C, M), **u8), sdhT=torch.empty((M // 128, C), **f32))
-    if "qaT" in want:
-        out.update(qaT=torch.empty((C // 2, M), **u8), saT=torch.empty((M // 128, C // 2), **f32))
+    with _allocating(stream):
+        if "dh" in want:
+            out["dh"] = torch.empty((M, C), dtype=torch.bfloat16, device=qh.device)
+        if "qdh" in want:
+            out.update(qdh=torch.empty((M, C), **u8), sdh=torch.empty((C // 128, M), **f32))
+        if "qdhT" in want:
+            out.update(qdhT=torch.empty((C, M), **u8), sdhT=torch.empty((M // 128, C), **f32))
+        if "qaT" in want:
+            out.update(qaT=torch.empty((C // 2, M), **u8), saT=torch.empty((M // 128, C // 2), **f32))
     fp8_swiglu_bwd(qh, sh, da, **out, scale_mode=scale_mode, stream=stream)
+    _handed_out(stream, *out.values())
     return out
 
 
@@ -622,8 +662,10 @@ def moe_mlp_few(x, topk, weights, W13, s13, W2, s2, out_dtype=None, scale_mode: 
     T, K = x.shape
     G, C, _ = W13.shape
     N = W2.shape[1]
-    out = torch.empty((T, N), dtype=out_dtype or torch.bfloat16, device=x.device)
     n = fp8_moe_mlp_few_workspace_bytes(T, topk.shape[-1], G, K, C // 2, N)
-    ws = torch.empty(max(n, 1), dtype=torch.uint8, device=x.device)
+    with _allocating(stream):
+        out = torch.empty((T, N), dtype=out_dtype or torch.bfloat16, device=x.device)
+        ws = torch.empty(max(n, 1), dtype=torch.uint8, device=x.device)
     fp8_moe_mlp_few(x, topk, weights, W13, s13, W2, s2, out, ws, scale_mode, stream)
+    _handed_out(stream, out)
     return out
