@@ -31,6 +31,9 @@ Dgrad and Wgrad all run in FP8; why-be.co.kr / cameseeing.com posts and
 "Three Fast Methods To Study Deepseek", Figure 7 (a): 1x128 / 128x128
 grouping; gnrental.net post: BF16 or FP32 GEMM outputs.)
 
+Constructors allocate on torch's current stream: a step that is called on
+another stream has to be ordered behind it first, as its inputs have to be.
+
 `kernel_calls` on each step counts the kernels one call launches.
 
 With scale_mode=SCALE_POW2 the dense steps accept tensor_core_scaling=True:
@@ -39,6 +42,8 @@ the GEMM then applies the power-of-two scales inside the tensor cores
 128-K partial in software.
 """
 from __future__ import annotations
+
+import contextlib
 
 import torch
 
@@ -356,22 +361,25 @@ class GatedMlpStep:
         fp8_blockscaled_gemm(self.qa, self.sa, self.qw2, self.sw2, self.y, B_KMAJOR, 128, cur)
         return self.y
 
-    def _gradient_buffers(self):
+    def _gradient_buffers(self, stream):
+        """Backward's buffers, allocated at its first call: on the stream it runs on (the side stream
+        is forked from that), so that memory still in use elsewhere is not taken."""
         if self._grad is None:
             M, K = self.x.shape
             N, I = self.w2.shape
             d, u8, f32 = self.x.device, torch.uint8, torch.float32
             if M % 128:
                 raise ValueError(f"backward needs whole groups of 128 tokens, got {M}")
-            self._grad = dict(
-                qdy=_empty((M, N), u8, d), sdy=_empty((N // 128, M), f32, d),
-                qdyT=_empty((N, M), u8, d), sdyT=_empty((M // 128, N), f32, d),
-                da=_empty((M, I), torch.bfloat16, d),
-                qdh=_empty((M, 2 * I), u8, d), sdh=_empty((2 * I // 128, M), f32, d),
-                qdhT=_empty((2 * I, M), u8, d), sdhT=_empty((M // 128, 2 * I), f32, d),
-                qaT=_empty((I, M), u8, d), saT=_empty((M // 128, I), f32, d),
-                qxT=_empty((K, M), u8, d), sxT=_empty((M // 128, K), f32, d),
-                dx=_empty((M, K), self.out_dtype, d), dw13=_empty((2 * I, K), f32, d), dw2=_empty((N, I), f32, d))
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                self._grad = dict(
+                    qdy=_empty((M, N), u8, d), sdy=_empty((N // 128, M), f32, d),
+                    qdyT=_empty((N, M), u8, d), sdyT=_empty((M // 128, N), f32, d),
+                    da=_empty((M, I), torch.bfloat16, d),
+                    qdh=_empty((M, 2 * I), u8, d), sdh=_empty((2 * I // 128, M), f32, d),
+                    qdhT=_empty((2 * I, M), u8, d), sdhT=_empty((M // 128, 2 * I), f32, d),
+                    qaT=_empty((I, M), u8, d), saT=_empty((M // 128, I), f32, d),
+                    qxT=_empty((K, M), u8, d), sxT=_empty((M // 128, K), f32, d),
+                    dx=_empty((M, K), self.out_dtype, d), dw13=_empty((2 * I, K), f32, d), dw2=_empty((N, I), f32, d))
         return self._grad
 
     def backward(self, dy, stream=None):
@@ -380,7 +388,7 @@ class GatedMlpStep:
         if dy.shape != self.y.shape or dy.device != self.y.device:
             raise ValueError(f"dy must have y's shape {tuple(self.y.shape)} and device {self.y.device}, "
                              f"got {tuple(dy.shape)} on {dy.device}")
-        g = self._gradient_buffers()
+        g = self._gradient_buffers(stream)
         cur, side = self._fork.begin(stream)
         # dy along tokens and x's cached codes regrouped, for the two Wgrads
         fp8_quant_act_128x1(dy, g["qdyT"], g["sdyT"], self.mode, side)
