@@ -350,7 +350,6 @@ class GatedMlpStep:
         self._ran = False
 
     def __call__(self, stream=None):
-        self._ran = True
         cur, side = self._fork.begin(stream)
         fp8_quant_w_128x128(self.w13, self.qw13, self.sw13, self.mode, side)
         fp8_quant_w_128x128(self.w2, self.qw2, self.sw2, self.mode, side)
@@ -359,6 +358,7 @@ class GatedMlpStep:
         fp8_blockscaled_gemm(self.qx, self.sx, self.qw13, self.sw13, self.h, B_KMAJOR, 128, cur)
         fp8_swiglu_quant(self.h, self.qa, self.sa, self.qh, self.sh, None, self.mode, cur)
         fp8_blockscaled_gemm(self.qa, self.sa, self.qw2, self.sw2, self.y, B_KMAJOR, 128, cur)
+        self._ran = True
         return self.y
 
     def _gradient_buffers(self, stream):

@@ -55,3 +55,15 @@ def test_gradient_buffers_belong_to_the_stream_that_first_uses_them(step):
     seen.clear()
     step.backward(dy, "main")
     assert not seen                    # kept from call to call
+
+
+def test_a_forward_pass_that_failed_does_not_count(step, monkeypatch):
+    step, _ = step
+
+    def refuse(*a, **k):
+        raise RuntimeError("refused")
+    monkeypatch.setattr(linear, "fp8_quant_w_128x128", refuse)
+    with pytest.raises(RuntimeError, match="refused"):
+        step("main")
+    with pytest.raises(RuntimeError, match="forward"):
+        step.backward(torch.zeros((128, 384)), "main")
