@@ -350,6 +350,7 @@ class GatedMlpStep:
         self._ran = False
 
     def __call__(self, stream=None):
+        self._ran = False
         cur, side = self._fork.begin(stream)
         fp8_quant_w_128x128(self.w13, self.qw13, self.sw13, self.mode, side)
         fp8_quant_w_128x128(self.w2, self.qw2, self.sw2, self.mode, side)

@@ -67,3 +67,17 @@ def test_a_forward_pass_that_failed_does_not_count(step, monkeypatch):
         step("main")
     with pytest.raises(RuntimeError, match="forward"):
         step.backward(torch.zeros((128, 384)), "main")
+
+
+def test_a_later_forward_pass_that_failed_takes_the_earlier_one_back(step, monkeypatch):
+    """It may have overwritten a part of what backward needs."""
+    step, _ = step
+    step("main")
+
+    def refuse(*a, **k):
+        raise RuntimeError("refused")
+    monkeypatch.setattr(linear, "fp8_swiglu_quant", refuse)
+    with pytest.raises(RuntimeError, match="refused"):
+        step("main")
+    with pytest.raises(RuntimeError, match="forward"):
+        step.backward(torch.zeros((128, 384)), "main")
