@@ -75,13 +75,37 @@ __device__ __forceinline__ float rcp_approx(float x)
 // codes of the forward, 320 (BF16 inputs) and 164 (FP32) differ from FP64's; with a Newton step on
 // the reciprocal and the argument's rounding made good it would be 293 and 145, for 3 to 14 % of
 // the time: not worth it, as one code in a million rounds the other way in FP32 whatever is done.
-// Below g = -87.3, where the reciprocal would be subnormal or exp(-g) overflows, the sigmoid
-// is 0, and so is the SiLU.
+//
+// For |g| <= kNearGates, where exp(-g) is below 2^126 and its reciprocal a normal number (ln(2^126) = 87.3).
+constexpr float kNearGates = 87.0f;
 __device__ __forceinline__ F2 sigmoid2(F2 g)
 {
     const F2 t = g * f2(-1.4426950408889634f, -1.4426950408889634f);      // -log2(e)
     const F2 y = f2(ex2_approx(lo(t)), ex2_approx(hi(t))) + f2(1.0f, 1.0f);
     return f2(rcp_approx(lo(y)), rcp_approx(hi(y)));
+}
+
+// The sigmoid of any finite gates, as a product r * f: below about -86.6, r stays at 2^-125 and f is
+// the rest, so that products with r first (g * r * f) are right down to FP32's smallest normal
+// number, where the sigmoid itself no longer is one; above, f is 1 and r has sigmoid2's bits. The
+// argument is kept where neither it nor what is made of it can overflow: the ends are 0 and 1.
+__device__ __forceinline__ void sigmoid2_far(F2 g, F2& r, F2& f)
+{
+    const F2 t = g * f2(-1.4426950408889634f, -1.4426950408889634f);
+    const float a = fminf(fmaxf(lo(t), -200.0f), 500.0f), b = fminf(fmaxf(hi(t), -200.0f), 500.0f);
+    const F2 y = f2(ex2_approx(fminf(a, 125.0f)), ex2_approx(fminf(b, 125.0f))) + f2(1.0f, 1.0f);
+    r = f2(rcp_approx(lo(y)), rcp_approx(hi(y)));
+    f = f2(ex2_approx(fminf(125.0f - a, 0.0f)), ex2_approx(fminf(125.0f - b, 0.0f)));
+}
+
+// silu(g) = g * sigmoid(g); FAR for any finite gates, else for |g| <= kNearGates (with the same bits there).
+template <bool FAR>
+__device__ __forceinline__ F2 silu2(F2 g)
+{
+    if (!FAR) return g * sigmoid2(g);
+    F2 r, f;
+    sigmoid2_far(g, r, f);
+    return g * r * f;
 }
 
 // max(|a|, |b|, |c|): one three-input instruction.

@@ -880,8 +880,11 @@ __global__ void __launch_bounds__(128) k_few_act(const Few f, uint32_t ctas)
             }
         }
 #pragma unroll
-        for (int i = 0; i < ACT_TOKENS; ++i)
-            g[i] = g[i] * rcp_approx(1.0f + ex2_approx(g[i] * -1.4426950408889634f)) * u[i];
+        for (int i = 0; i < ACT_TOKENS; i += 2) {
+            const F2 a = silu2<true>(f2(g[i], g[i + 1])) * f2(u[i], u[i + 1]);
+            g[i] = lo(a);
+            g[i + 1] = hi(a);
+        }
 #pragma unroll
         for (int i = 0; i < ACT_TOKENS; ++i) {
             const float m = warp_absmax(g[i]);
@@ -968,7 +971,7 @@ __global__ void __launch_bounds__(128) k_few_act_rows(const Few f, uint32_t ctas
         float m = 0.0f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            g[i] = g[i] * sigmoid2(g[i]) * u[i];
+            g[i] = silu2<true>(g[i]) * u[i];
             m = absmax3(m, lo(g[i]), hi(g[i]));
         }
         __syncthreads();                      // (the round before has read wmax)

@@ -21,6 +21,7 @@
 #include <cstddef>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "fp8fg_device.cuh"
 #include "fp8fg_host.h"
@@ -249,11 +250,17 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdCtasPerSm) k_swiglu_quant(
         F2 g[8], u[8], a[8];
         rg[i].get(g);
         ru[i].get(u);
+        const float gmax = absmax16(g);
+        if (__any_sync(0xffffffffu, gmax > kNearGates)) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] = g[j] * sigmoid2(g[j]) * u[j];
+            for (int j = 0; j < 8; ++j) a[j] = silu2<true>(g[j]) * u[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a[j] = silu2<false>(g[j]) * u[j];
+        }
         float mine = row_max(absmax16(a));
         if (KEEP) {
-            const float mg = row_max(absmax16(g)), mu = row_max(absmax16(u));
+            const float mg = row_max(gmax), mu = row_max(absmax16(u));
             mine = l == 1 ? mg : (l == 2 ? mu : mine);
         }
         const GroupScale gs = group_scale(mine, mode);
@@ -296,16 +303,29 @@ constexpr int kBwdThreads = 512;
 constexpr int kBwdWarps = kBwdThreads / 32;     // 16
 constexpr int kBwdTok = 128 / kBwdWarps;        // 8 tokens per warp
 
-// dG, dU and a of a pair of channels.
+// dG, dU and a of a pair of channels (FAR as in silu2).
+template <bool FAR>
 __device__ __forceinline__ void gradients(F2 g, F2 u, F2 da, F2& dg, F2& du, F2& a)
 {
     const F2 one = f2(1.0f, 1.0f);
-    const F2 sig = sigmoid2(g), silu = g * sig;
-    const F2 rest = fma2(sig, f2(-1.0f, -1.0f), one);              // 1 - s
-    dg = da * u * (sig * fma2(g, rest, one));
+    F2 r, f;
+    if (FAR)
+        sigmoid2_far(g, r, f);
+    else
+        r = sigmoid2(g);
+    const F2 rest = fma2(FAR ? r * f : r, f2(-1.0f, -1.0f), one);      // 1 - s
+    F2 silu = g * r, slope = r * fma2(g, rest, one);
+    if (FAR) {
+        silu = silu * f;
+        slope = slope * f;
+    }
+    dg = da * u * slope;
     du = da * silu;
     a = silu * u;
 }
+
+// Whether gates of checkpoints with these scales may lie beyond kNearGates (a code is at most 448).
+__device__ __forceinline__ bool far_gates(float scale) { return !(fabsf(scale) <= kNearGates / 448.0f); }
 
 // Backward without transposed outputs: no group spans rows, so the work is split as the forward's (8
 // lanes own a row's channel block).  16384 x 2048, codes of dH alone: 35.7 us (FP32 dA 43.9), 46.6
@@ -351,18 +371,24 @@ __global__ void __launch_bounds__(kFwdThreads, kBwdRowsCtasPerSm) k_swiglu_bwd_r
         F2 da[8], dg[8], du[8];
         rd[i].get(da);
         const F2 s0 = f2(sg[i], sg[i]), s1 = f2(su[i], su[i]);
+        auto all = [&](auto far) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float gf[4], uf[4];
-            decode4_e4m3(cg[i][j], gf);
-            decode4_e4m3(cu[i][j], uf);
+            for (int j = 0; j < 4; ++j) {
+                float gf[4], uf[4];
+                decode4_e4m3(cg[i][j], gf);
+                decode4_e4m3(cu[i][j], uf);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                F2 a;
-                gradients(f2(gf[2 * k], gf[2 * k + 1]) * s0, f2(uf[2 * k], uf[2 * k + 1]) * s1, da[2 * j + k],
-                          dg[2 * j + k], du[2 * j + k], a);
+                for (int k = 0; k < 2; ++k) {
+                    F2 a;
+                    gradients<decltype(far)::value>(f2(gf[2 * k], gf[2 * k + 1]) * s0, f2(uf[2 * k], uf[2 * k + 1]) * s1,
+                                                    da[2 * j + k], dg[2 * j + k], du[2 * j + k], a);
+                }
             }
-        }
+        };
+        if (__any_sync(0xffffffffu, far_gates(sg[i])))
+            all(std::true_type{});
+        else
+            all(std::false_type{});
         if (p.dh && live) {
             __nv_bfloat16* dst = p.dh + (int64_t)(int)m * p.lddh + col;
             V::store_bf16(dst, dg);
@@ -570,24 +596,34 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
             for (int i = 0; i < 2 * kBwdTok; i += 4)
                 *reinterpret_cast<float4*>(&sc[0][0] + i) =
                     *reinterpret_cast<const float4*>(&d.scale[i / kBwdTok][w * kBwdTok + i % kBwdTok]);
+            auto all = [&](auto far) {
 #pragma unroll
-            for (int i = 0; i < kBwdTok; ++i) {
-                const int r = w * kBwdTok + i;
-                const float s0 = sc[0][i], s1 = sc[1][i];
-                float gf[4], uf[4];
-                decode4_e4m3(*reinterpret_cast<const uint32_t*>(d.g + r * 128 + 4 * lane), gf);
-                decode4_e4m3(*reinterpret_cast<const uint32_t*>(d.u + r * 128 + 4 * lane), uf);
-                Quad<Tda> q;
-                q.load_shared(d.da + r * 128 + 4 * lane);
-                F2 da[2];
-                q.get(da[0], da[1]);
-                const F2 sg = f2(s0, s0), su = f2(s1, s1);
+                for (int i = 0; i < kBwdTok; ++i) {
+                    const int r = w * kBwdTok + i;
+                    const float s0 = sc[0][i], s1 = sc[1][i];
+                    float gf[4], uf[4];
+                    decode4_e4m3(*reinterpret_cast<const uint32_t*>(d.g + r * 128 + 4 * lane), gf);
+                    decode4_e4m3(*reinterpret_cast<const uint32_t*>(d.u + r * 128 + 4 * lane), uf);
+                    Quad<Tda> q;
+                    q.load_shared(d.da + r * 128 + 4 * lane);
+                    F2 da[2];
+                    q.get(da[0], da[1]);
+                    const F2 sg = f2(s0, s0), su = f2(s1, s1);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    gradients(f2(gf[2 * k], gf[2 * k + 1]) * sg, f2(uf[2 * k], uf[2 * k + 1]) * su, da[k], v[0][i][k],
-                              v[1][i][k], v[2][i][k]);
+                    for (int k = 0; k < 2; ++k) {
+                        gradients<decltype(far)::value>(f2(gf[2 * k], gf[2 * k + 1]) * sg,
+                                                        f2(uf[2 * k], uf[2 * k + 1]) * su, da[k], v[0][i][k], v[1][i][k],
+                                                        v[2][i][k]);
+                    }
                 }
-            }
+            };
+            bool far = false;
+#pragma unroll
+            for (int i = 0; i < kBwdTok; ++i) far |= far_gates(sc[0][i]);
+            if (far)
+                all(std::true_type{});
+            else
+                all(std::false_type{});
         }
 
         // per-warp column maxima for the 128x1 groups
