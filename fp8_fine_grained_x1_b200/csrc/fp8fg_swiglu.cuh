@@ -69,20 +69,27 @@ __device__ __forceinline__ float rcp_approx(float x)
     return r;
 }
 
-// The SwiGLU's exponential and reciprocal are the hardware's approximations, each
-// within a few units in the last place of FP32, and the roundings of log2(e) and of
-// g * log2(e) add up to |g| * 2^-23 to exp(-g)'s relative error.  Of 2 x 10^8
-// codes of the forward, 320 (BF16 inputs) and 164 (FP32) differ from FP64's; with a Newton step on
-// the reciprocal and the argument's rounding made good it would be 293 and 145, for 3 to 14 % of
-// the time: not worth it, as one code in a million rounds the other way in FP32 whatever is done.
+// 1 / (1 + exp(-g)).  exp(-g) is 2^t for t = -g * log2(e), rounded: that alone would cost |g| * 2^-23 of it
+// (the product's rounding, and log2(e)'s).  What is lost, -g - t * ln(2), is exact in one FMA but for
+// ln(2)'s rounding (2^-28.4 of it), and exp(-g) = 2^t * (1 + that) to FP32's precision.  The
+// exponential and the reciprocal are the hardware's approximations, at most two and one units in the last
+// place off.
 //
+// The reciprocal of 1 + e * (1 + what is lost).
+__device__ __forceinline__ F2 rcp_1p_exp(F2 e, F2 t, F2 g)
+{
+    const F2 minus = f2(-1.0f, -1.0f), d = fma2(t, f2(0.6931471805599453f, 0.6931471805599453f), g);
+    const F2 y = fma2(e, d, fma2(e, minus, minus));      // negated, as d is minus what is lost
+    return f2(rcp_approx(-lo(y)), rcp_approx(-hi(y)));
+}
+
 // For |g| <= kNearGates, where exp(-g) is below 2^126 and its reciprocal a normal number (ln(2^126) = 87.3).
 constexpr float kNearGates = 87.0f;
 __device__ __forceinline__ F2 sigmoid2(F2 g)
 {
     const F2 t = g * f2(-1.4426950408889634f, -1.4426950408889634f);      // -log2(e)
-    const F2 y = f2(ex2_approx(lo(t)), ex2_approx(hi(t))) + f2(1.0f, 1.0f);
-    return f2(rcp_approx(lo(y)), rcp_approx(hi(y)));
+    const F2 e = f2(ex2_approx(lo(t)), ex2_approx(hi(t)));
+    return rcp_1p_exp(e, t, g);
 }
 
 // The sigmoid of any finite gates, as a product r * f: below about -86.6, r stays at 2^-125 and f is
@@ -93,8 +100,8 @@ __device__ __forceinline__ void sigmoid2_far(F2 g, F2& r, F2& f)
 {
     const F2 t = g * f2(-1.4426950408889634f, -1.4426950408889634f);
     const float a = fminf(fmaxf(lo(t), -200.0f), 500.0f), b = fminf(fmaxf(hi(t), -200.0f), 500.0f);
-    const F2 y = f2(ex2_approx(fminf(a, 125.0f)), ex2_approx(fminf(b, 125.0f))) + f2(1.0f, 1.0f);
-    r = f2(rcp_approx(lo(y)), rcp_approx(hi(y)));
+    const F2 e = f2(ex2_approx(fminf(a, 125.0f)), ex2_approx(fminf(b, 125.0f)));
+    r = rcp_1p_exp(e, f2(a, b), g);
     f = f2(ex2_approx(fminf(125.0f - a, 0.0f)), ex2_approx(fminf(125.0f - b, 0.0f)));
 }
 

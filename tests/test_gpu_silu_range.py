@@ -18,7 +18,7 @@ import torch
 import fp8_fine_grained_x1_b200 as fg
 from oracle import mlp
 
-from gpu_util import dev, to_dev
+from gpu_util import dev, half_ulp_bf16, to_dev
 
 pytestmark = pytest.mark.gpu
 
@@ -49,6 +49,63 @@ def _cols_ok(qT, s, v, err, mode):
     S = np.repeat(s.astype(np.float64), 128, axis=0)
     assert mlp.scale_error(s, amax(v), amax(err), mode) <= 2.0 ** -22
     assert mlp.code_excess(qT.T, S, v, err) <= 0.0
+
+
+def _gates(kind, shape, rng):
+    """`low` ends where silu(g) is still normal; `around` lies on both sides of ln(2^126) = 87.34."""
+    lo, hi = dict(moderate=(-20.0, -8.0), far=(-85.0, -60.0), around=(-88.5, -86.0), low=(-91.5, -87.5))[kind]
+    return rng.uniform(lo, hi, shape)
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("kind", ["moderate", "far", "around", "low"])
+def test_forward(kind, dtype, mode):
+    M, I = 200, 256
+    rng = np.random.default_rng(1)
+    h = np.concatenate((_gates(kind, (M, I), rng), rng.normal(0, 1e10, (M, I))), 1).astype(np.float32)
+    x = to_dev(h)
+    if dtype == "bf16":
+        x = x.to(torch.bfloat16)
+    val = x.double().cpu().numpy()
+    a = mlp.swiglu(val)
+    for keep in (True, False):
+        qa, sa, _, _ = fg.swiglu_quant(x, keep, mode)
+        _rows_ok(_np(qa), _np(sa), a, ACT * np.abs(a), mode)
+
+
+def _codes(values):
+    """E4M3 codes of values that the format holds."""
+    table = {float(mlp.decode(np.uint8(c))): c for c in range(256) if c not in (0x7F, 0xFF)}
+    return np.vectorize(table.__getitem__, otypes=[np.uint8])(values)
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("scale,codes", [(91.5 / 448, (-448, -416)), (91.5 / 448, (-448, -416, -384, -288)),
+                                         (0.25, (-352, -344 + 24)), (0.03, (-448, -416, -352))])
+def test_backward(scale, codes, dtype, mode):
+    """Gates that are codes times a scale: -91.5 .. -58, -88 and -80, -13.4 .. -10.6."""
+    M, I = 256, 256
+    rng = np.random.default_rng(2)
+    q = np.concatenate((_codes(rng.choice(np.array(codes, np.float64), (M, I))),
+                        rng.choice(np.array([0x38, 0x40, 0x7E, 0xB9, 0xF0], np.uint8), (M, I))), 1)
+    s = np.concatenate((np.full((I // 128, M), scale), np.full((I // 128, M), 1e8))).astype(np.float32)
+    h = _decoded(q, s)
+    da = to_dev(rng.normal(0, 1e20, (M, I)).astype(np.float32))
+    da = da.to(torch.bfloat16) if dtype == "bf16" else da
+    dv = da.double().cpu().numpy()
+    dh, mag = mlp.swiglu_grads(h, dv)
+    a = mlp.swiglu(h)
+    out = fg.swiglu_bwd(to_dev(q), to_dev(s), da, ("dh", "qdh", "qdhT", "qaT"), mode)
+    got = out["dh"].double().cpu().numpy()
+    assert np.all(np.abs(got - dh) <= half_ulp_bf16(np.maximum(np.abs(dh), np.abs(got))) + GRAD * mag)
+    _rows_ok(_np(out["qdh"]), _np(out["sdh"]), dh, GRAD * mag, mode)
+    _cols_ok(_np(out["qdhT"]), _np(out["sdhT"]), dh, GRAD * mag, mode)
+    _cols_ok(_np(out["qaT"]), _np(out["saT"]), a, ACT * np.abs(a), mode)
+    rows = fg.swiglu_bwd(to_dev(q), to_dev(s), da, ("dh", "qdh"), mode)      # the kernel without operands along tokens
+    assert torch.equal(rows["dh"], out["dh"]) and torch.equal(rows["qdh"], out["qdh"])
+    assert torch.equal(rows["sdh"], out["sdh"])
 
 
 EXTREME = [3.3e38, 2.5e38, 1e38, 1e30, 200.0, 104.0, 88.0, 87.0, 86.0, 1.0, 1e-30, 0.0, -1e-30, -1.0, -86.0, -87.0, -88.0,
