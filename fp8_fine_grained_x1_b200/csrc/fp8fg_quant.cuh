@@ -54,11 +54,12 @@ __device__ __forceinline__ GroupScale group_scale(float amax, int mode)
         return g;
     }
     // Both quotients correctly rounded.  Where nothing can under- or overflow they come from the
-    // correctly rounded reciprocals r of 448 and of amax: q = fl(x * r) is within a unit in the
-    // last place of x / y, the remainder x - q * y is then exact in one FMA, and
-    // fl(q + remainder * r) is the correctly rounded quotient (Markstein's theorem, "Computation
-    // of elementary functions on the IBM RISC System/6000 processor", 1990; compared with
-    // __fdiv_rn for every FP32 value of this range).  About half the instructions of two divisions.
+    // correctly rounded reciprocals r of 448 and of amax: q = fl(x * r), the remainder x - q * y in one FMA,
+    // and fl(q + remainder * r), the steps of Markstein's division ("Computation of elementary functions on
+    // the IBM RISC System/6000 processor", 1990).  His theorem wants q within one unit in the last place, and q
+    // is up to 1.4 off here; that the results are the correctly rounded quotients all the same is shown by
+    // exhaustion, over all 2^23 significands (a power of two in amax changes no step).  About half the
+    // instructions of two divisions.
     if (__float_as_uint(amax) - 0x0F800000u <= 0x60000000u) {      // 2^-96 <= amax <= 2^96
         constexpr float r448 = 1.0f / 448.0f;
         const float q = amax * r448;
