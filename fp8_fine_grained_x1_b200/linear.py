@@ -319,14 +319,20 @@ class GatedMlpStep:
 
     Calling the step runs the forward pass and returns Y.  `backward(dy)` (dy
     [M, N] BF16 or FP32, M a multiple of 128) returns dX (out_dtype), dW13 and
-    dW2 (FP32).  Between the two the step keeps, in FP8, X's 1x128 codes and H's
-    (`qx`, `qh`: 3 bytes per token and channel of K and of I where BF16 X, H and A
-    would take 2 K + 6 I); H in BF16 is scratch, and A is recomputed.  Weights are
-    quantized in the forward pass and reused by backward."""
+    dW2 (FP32).  Between the two the step needs, in FP8, X's 1x128 codes and H's
+    (`qx`, `qh`: K + 2 I bytes a token and their scales, where BF16 X, H and A would
+    take 2 K + 6 I); A is recomputed.  Weights are quantized in the forward pass and
+    reused by backward.
+
+    H in BF16, A's codes and the operands of backward's GEMMs are scratch.  Each step
+    has its own unless it is given another's: `share` is a step of the same sizes
+    (another layer) whose scratch this one uses too, so that a model of many layers
+    holds it once.  Steps that share run one after the other, in any order of
+    forward and backward passes."""
     kernel_calls = 6             # x, w13, w2 quantizers, two GEMMs, the SwiGLU
     kernel_calls_backward = 8    # dy twice, cached x, the SwiGLU, four GEMMs
 
-    def __init__(self, x, w13, w2, out_dtype=torch.bfloat16, scale_mode=SCALE_FP32):
+    def __init__(self, x, w13, w2, out_dtype=torch.bfloat16, scale_mode=SCALE_FP32, share=None):
         M, K = x.shape
         C, K2 = w13.shape
         N, I = w2.shape
@@ -339,9 +345,16 @@ class GatedMlpStep:
         self.qx, self.sx = _empty((M, K), u8, d), _empty((K // 128, M), f32, d)
         self.qw13, self.sw13 = _empty((C, K), u8, d), _empty((C // 128, K // 128), f32, d)
         self.qw2, self.sw2 = _empty((N, I), u8, d), _empty((N // 128, I // 128), f32, d)
-        self.h = _empty((M, C), torch.bfloat16, d)
         self.qh, self.sh = _empty((M, C), u8, d), _empty((C // 128, M), f32, d)
-        self.qa, self.sa = _empty((M, I), u8, d), _empty((I // 128, M), f32, d)
+        if share is None:
+            self._scratch = dict(sizes=(M, K, I, N, d), h=_empty((M, C), torch.bfloat16, d), qa=_empty((M, I), u8, d),
+                                 sa=_empty((I // 128, M), f32, d), grad=None)
+        else:
+            if share._scratch["sizes"] != (M, K, I, N, d):
+                raise ValueError(f"share: a step of (M, K, I, N, device) = {share._scratch['sizes']}, this one has "
+                                 f"{(M, K, I, N, d)}")
+            self._scratch = share._scratch
+        self.h, self.qa, self.sa = (self._scratch[n] for n in ("h", "qa", "sa"))
         self.y = _empty((M, N), out_dtype, d)
         self.flops = 2 * M * (C * K + N * I)
         self.inputs, self.output = [x, w13, w2], self.y
@@ -372,14 +385,17 @@ class GatedMlpStep:
             if M % 128:
                 raise ValueError(f"backward needs whole groups of 128 tokens, got {M}")
             with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                if self._scratch["grad"] is None:
+                    self._scratch["grad"] = dict(
+                        qdy=_empty((M, N), u8, d), sdy=_empty((N // 128, M), f32, d),
+                        qdyT=_empty((N, M), u8, d), sdyT=_empty((M // 128, N), f32, d),
+                        da=_empty((M, I), torch.bfloat16, d),
+                        qdh=_empty((M, 2 * I), u8, d), sdh=_empty((2 * I // 128, M), f32, d),
+                        qdhT=_empty((2 * I, M), u8, d), sdhT=_empty((M // 128, 2 * I), f32, d),
+                        qaT=_empty((I, M), u8, d), saT=_empty((M // 128, I), f32, d),
+                        qxT=_empty((K, M), u8, d), sxT=_empty((M // 128, K), f32, d))
                 self._grad = dict(
-                    qdy=_empty((M, N), u8, d), sdy=_empty((N // 128, M), f32, d),
-                    qdyT=_empty((N, M), u8, d), sdyT=_empty((M // 128, N), f32, d),
-                    da=_empty((M, I), torch.bfloat16, d),
-                    qdh=_empty((M, 2 * I), u8, d), sdh=_empty((2 * I // 128, M), f32, d),
-                    qdhT=_empty((2 * I, M), u8, d), sdhT=_empty((M // 128, 2 * I), f32, d),
-                    qaT=_empty((I, M), u8, d), saT=_empty((M // 128, I), f32, d),
-                    qxT=_empty((K, M), u8, d), sxT=_empty((M // 128, K), f32, d),
+                    self._scratch["grad"],
                     dx=_empty((M, K), self.out_dtype, d), dw13=_empty((2 * I, K), f32, d), dw2=_empty((N, I), f32, d))
         return self._grad
 

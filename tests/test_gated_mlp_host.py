@@ -81,3 +81,57 @@ def test_a_later_forward_pass_that_failed_takes_the_earlier_one_back(step, monke
         step("main")
     with pytest.raises(RuntimeError, match="forward"):
         step.backward(torch.zeros((128, 384)), "main")
+
+
+def _bytes(*steps):
+    """Bytes that the steps hold in tensors of their own (not their inputs), each storage counted once."""
+    seen = {}
+    for s in steps:
+        own = [v for v in vars(s).values() if torch.is_tensor(v)] + [v for v in (s._grad or {}).values()]
+        inputs = {t.data_ptr() for t in s.inputs}
+        seen.update({t.data_ptr(): t.numel() * t.element_size() for t in own if t.data_ptr() not in inputs})
+    return sum(seen.values())
+
+
+def test_steps_share_their_scratch(step):
+    """A further layer adds what it has to keep (FP8 checkpoints, FP8 weights) and hand out (Y and the gradients)."""
+    first, _ = step
+    M, K, I, N = 128, 256, 256, 384
+    dy = torch.zeros((M, N))
+    second = linear.GatedMlpStep(torch.zeros((M, K)), torch.zeros((2 * I, K)), torch.zeros((N, I)), share=first)
+    third = linear.GatedMlpStep(torch.zeros((M, K)), torch.zeros((2 * I, K)), torch.zeros((N, I)), share=second)
+    for s in (first, second, third):
+        s("main")
+    for s in (third, first, second):
+        s.backward(dy, "main")
+    keep = M * (K + 2 * I) + 4 * M * (K + 2 * I) // 128
+    weights = (2 * I * K + N * I) + 4 * (2 * I * K + N * I) // 128 ** 2
+    hand_out = 2 * M * N + 2 * M * K + 4 * (2 * I * K + N * I)
+    assert _bytes(first, second, third) - _bytes(first, second) == keep + weights + hand_out
+    for other in (torch.zeros((256, K)), None):
+        with pytest.raises(ValueError, match="share"):
+            if other is not None:
+                linear.GatedMlpStep(other, torch.zeros((2 * I, K)), torch.zeros((N, I)), share=first)
+            else:
+                linear.GatedMlpStep(torch.zeros((M, K)), torch.zeros((2 * I, K)), torch.zeros((N + 128, I)), share=first)
+
+
+@pytest.mark.gpu
+def test_layers_that_share_give_the_bits_of_layers_that_do_not():
+    from fp8_fine_grained_x1_b200 import synth
+    d = torch.device("cuda", 0)
+    M, K, I = 256, 256, 384
+    w = [(synth.normal((2 * I, K), K ** -0.5, 2 + i).to(d), synth.normal((K, I), I ** -0.5, 7 + i).to(d)) for i in range(3)]
+    dy = synth.normal((M, K), 1e-3, 4).to(d)
+    results = []
+    for shared in (False, True):
+        x, steps = synth.activations(M, K, seed=1).to(d), []
+        for w13, w2 in w:
+            steps.append(linear.GatedMlpStep(x, w13, w2, share=steps[0] if shared and steps else None))
+            x = steps[-1]()
+        g, out = dy, [x.clone()]
+        for s in reversed(steps):
+            g, dw13, dw2 = s.backward(g)
+            out += [g.clone(), dw13.clone(), dw2.clone()]
+        results.append(out)
+    assert all(torch.equal(a, b) for a, b in zip(*results))
