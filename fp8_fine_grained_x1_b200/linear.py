@@ -324,15 +324,21 @@ class GatedMlpStep:
     take 2 K + 6 I); A is recomputed.  Weights are quantized in the forward pass and
     reused by backward.
 
-    H in BF16, A's codes and the operands of backward's GEMMs are scratch.  Each step
+    H and dA are rounded to `hidden_dtype` between the GEMMs and the SwiGLU: to BF16
+    unless FP32 is asked for, which keeps their sums as they are for 4 bytes an element
+    more on the way (BF16 halves that traffic, and the E4M3 codes made of them keep 4
+    bits of significand where BF16 has 8).
+
+    H, A's codes and the operands of backward's GEMMs are scratch.  Each step
     has its own unless it is given another's: `share` is a step of the same sizes
     (another layer) whose scratch this one uses too, so that a model of many layers
-    holds it once.  Steps that share run one after the other, in any order of
+    holds it once (with hidden_dtype the same).  Steps that share run one after the other, in any order of
     forward and backward passes."""
     kernel_calls = 6             # x, w13, w2 quantizers, two GEMMs, the SwiGLU
     kernel_calls_backward = 8    # dy twice, cached x, the SwiGLU, four GEMMs
 
-    def __init__(self, x, w13, w2, out_dtype=torch.bfloat16, scale_mode=SCALE_FP32, share=None):
+    def __init__(self, x, w13, w2, out_dtype=torch.bfloat16, scale_mode=SCALE_FP32, share=None,
+                 hidden_dtype=torch.bfloat16):
         M, K = x.shape
         C, K2 = w13.shape
         N, I = w2.shape
@@ -347,12 +353,12 @@ class GatedMlpStep:
         self.qw2, self.sw2 = _empty((N, I), u8, d), _empty((N // 128, I // 128), f32, d)
         self.qh, self.sh = _empty((M, C), u8, d), _empty((C // 128, M), f32, d)
         if share is None:
-            self._scratch = dict(sizes=(M, K, I, N, d), h=_empty((M, C), torch.bfloat16, d), qa=_empty((M, I), u8, d),
-                                 sa=_empty((I // 128, M), f32, d), grad=None)
+            self._scratch = dict(sizes=(M, K, I, N, hidden_dtype, d), h=_empty((M, C), hidden_dtype, d),
+                                 qa=_empty((M, I), u8, d), sa=_empty((I // 128, M), f32, d), grad=None)
         else:
-            if share._scratch["sizes"] != (M, K, I, N, d):
-                raise ValueError(f"share: a step of (M, K, I, N, device) = {share._scratch['sizes']}, this one has "
-                                 f"{(M, K, I, N, d)}")
+            if share._scratch["sizes"] != (M, K, I, N, hidden_dtype, d):
+                raise ValueError(f"share: a step of (M, K, I, N, hidden_dtype, device) = {share._scratch['sizes']}, "
+                                 f"this one has {(M, K, I, N, hidden_dtype, d)}")
             self._scratch = share._scratch
         self.h, self.qa, self.sa = (self._scratch[n] for n in ("h", "qa", "sa"))
         self.y = _empty((M, N), out_dtype, d)
@@ -389,7 +395,7 @@ class GatedMlpStep:
                     self._scratch["grad"] = dict(
                         qdy=_empty((M, N), u8, d), sdy=_empty((N // 128, M), f32, d),
                         qdyT=_empty((N, M), u8, d), sdyT=_empty((M // 128, N), f32, d),
-                        da=_empty((M, I), torch.bfloat16, d),
+                        da=_empty((M, I), self.h.dtype, d),
                         qdh=_empty((M, 2 * I), u8, d), sdh=_empty((2 * I // 128, M), f32, d),
                         qdhT=_empty((2 * I, M), u8, d), sdhT=_empty((M // 128, 2 * I), f32, d),
                         qaT=_empty((I, M), u8, d), saT=_empty((M // 128, I), f32, d),
@@ -429,14 +435,14 @@ class MoeMlpStep:
     Up to MOE_FEW_MAX_TOKENS tokens take one call that reads each active
     expert's weights once (fp8_moe_mlp_few).  More tokens are quantized and
     dispatched to 128-padded groups, and the SwiGLU between the two grouped GEMMs
-    quantizes the rows in use for the second; H is BF16 there and FP32 in the
-    few-token form.  On 32 experts of 7168 x 2048, top-8, the few-token form took
+    quantizes the rows in use for the second; H is `hidden_dtype` there (BF16 unless
+    FP32 is asked for) and FP32 in the few-token form.  On 32 experts of 7168 x 2048, top-8, the few-token form took
     70, 196, 240, 249 and 272 us for 1, 8, 32, 64 and 128 tokens, the dispatched
     form 177, 389, 461, 496 and 512: it is taken wherever it can be.  `few`
     overrides the choice."""
 
     def __init__(self, x, topk, weights, qw13, sw13, qw2, sw2, out_dtype=torch.bfloat16, scale_mode=SCALE_FP32,
-                 few=None):
+                 few=None, hidden_dtype=torch.bfloat16):
         T, K = x.shape
         k = topk.shape[1]
         G, C, _ = qw13.shape
@@ -464,7 +470,7 @@ class MoeMlpStep:
         self.token_row = _empty((T, k), torch.int32, d)
         self.row_token = _empty((M,), torch.int32, d)
         self.ws = _empty((max(1, fp8_moe_dispatch_workspace_bytes(T, k, G) // 4),), torch.int32, d)
-        self.h = _empty((M, C), torch.bfloat16, d)
+        self.h = _empty((M, C), hidden_dtype, d)
         self.qa, self.sa = _empty((M, I), u8, d), _empty((I // 128, M), f32, d)
         self.y = _empty((M, N), torch.bfloat16, d)
 
