@@ -53,7 +53,8 @@ EXPORTED = (
     "fp8_moe_dispatch_noalloc", "fp8_requant_1x128_to_128x1", "fp8_blockscaled_gemm_pow2",
     "fp8_grouped_gemm_pow2", "fp8_moe_quant_dispatch", "fp8_selftest_gemm_unwind",
     "fp8_grouped_gemm_gather", "fp8_moe_route", "fp8_swiglu_quant", "fp8_swiglu_bwd",
-    "fp8_moe_mlp_few_workspace_bytes", "fp8_moe_mlp_few",
+    "fp8_moe_mlp_few_workspace_bytes", "fp8_moe_mlp_few", "fp8_selftest_swiglu_bwd_unwind",
+    "fp8_selftest_moe_mlp_few_unwind",
 )
 
 MOE_FEW_MAX_TOKENS = 128     # FP8_MOE_FEW_MAX_TOKENS
@@ -137,6 +138,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fp8_moe_mlp_few.argtypes = [_P, _I, _I64, _I64, _I64, _P, _P, _I, _I, _P, _P, _P, _P, _I64,
                                     _I64, _P, _I, _I64, _P, _I64, _I, _P]
     lib.fp8_moe_mlp_few.restype = _I
+    lib.fp8_selftest_swiglu_bwd_unwind.argtypes = [_P, _P, _P, _I, _I64, _I64, _P, _P, _P]
+    lib.fp8_selftest_swiglu_bwd_unwind.restype = _I
+    lib.fp8_selftest_moe_mlp_few_unwind.argtypes = [_I, _P, _I, _I64, _I64, _P, _P, _I, _I, _P, _P, _P, _P,
+                                                    _I64, _I64, _P, _I, _P, _I64, _P]
+    lib.fp8_selftest_moe_mlp_few_unwind.restype = _I
     _lib = lib
     return lib
 
@@ -498,6 +504,28 @@ def fp8_selftest_gemm_unwind(kernel: int, A, sA, B, sB, D, group_offsets=None,
     _check(load_library().fp8_selftest_gemm_unwind(
         kernel, _ptr(A), _ptr(sA), _ptr(B), _ptr(sB), _ptr(group_offsets), G, M, N, K, _ptr(D),
         _out_dtype(D), _stream(stream)), "fp8_selftest_gemm_unwind")
+
+
+def fp8_selftest_swiglu_bwd_unwind(qh, sh, da, qdhT, sdhT, stream=None) -> None:
+    """Launch the SwiGLU backward for operands along tokens with one warp of every CTA withholding its
+    first hand-over, so that its waits run out (FP8_ERR_TIMEOUT in the status)."""
+    M, I = da.shape
+    d, u8, f32 = qh.get_device(), qh.dtype, sh.dtype
+    _call_on(d, stream, load_library().fp8_selftest_swiglu_bwd_unwind, "fp8_selftest_swiglu_bwd_unwind",
+             _flat(qh, "qh", u8, (M, 2 * I), d), _flat(sh, "sh", f32, (2 * I // 128, M), d),
+             _flat(da, "da", da.dtype, (M, I), d), _in_dtype(da), M, I, _flat(qdhT, "qdhT", u8, (2 * I, M), d),
+             _flat(sdhT, "sdhT", f32, (M // 128, 2 * I), d))
+
+
+def fp8_selftest_moe_mlp_few_unwind(phase, x, topk, weights, W13, s13, W2, s2, out, workspace, stream=None) -> None:
+    """Launch fp8_moe_mlp_few with every CTA of phase 1 or 2 holding back its first unit's token rows, so
+    that its waits run out (FP8_ERR_TIMEOUT in the status)."""
+    T, K = x.shape
+    G, C, _ = W13.shape
+    N = W2.shape[1]
+    _call_on(x.get_device(), stream, load_library().fp8_selftest_moe_mlp_few_unwind, "fp8_selftest_moe_mlp_few_unwind",
+             phase, _ptr(x), _in_dtype(x), T, K, _ptr(topk), _ptr(weights), topk.shape[1], G, _ptr(W13), _ptr(s13),
+             _ptr(W2), _ptr(s2), C // 2, N, _ptr(out), _out_dtype(out), _ptr(workspace), workspace.numel())
 
 
 def fp8_device_supported() -> bool:

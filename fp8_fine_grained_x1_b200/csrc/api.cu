@@ -427,11 +427,11 @@ FP8FG_API int64_t fp8_moe_mlp_few_workspace_bytes(int64_t T, int k, int G, int64
     return few_shape_ok(T, k, G, K, I, N) ? moe_mlp_few_workspace_bytes(T, k, G, K, I, N) : 0;
 }
 
-FP8FG_API int fp8_moe_mlp_few(const void* x, int in_dtype, int64_t T, int64_t K, int64_t ldx,
-                              const int32_t* topk, const float* weights, int k, int G, const uint8_t* W13,
-                              const float* s13, const uint8_t* W2, const float* s2, int64_t I, int64_t N,
-                              void* out, int out_dtype, int64_t ldo, void* workspace,
-                              int64_t workspace_bytes, int scale_mode, void* stream)
+static int moe_mlp_few(const void* x, int in_dtype, int64_t T, int64_t K, int64_t ldx, const int32_t* topk,
+                       const float* weights, int k, int G, const uint8_t* W13, const float* s13,
+                       const uint8_t* W2, const float* s2, int64_t I, int64_t N, void* out, int out_dtype,
+                       int64_t ldo, void* workspace, int64_t workspace_bytes, int scale_mode, void* stream,
+                       int withhold)
 {
     if (!is_in(in_dtype) || !is_out(out_dtype) || !is_mode(scale_mode)) return FP8_ERR_DTYPE;
     if (!few_shape_ok(T, k, G, K, I, N) || ldx < K || ldx > kMaxDim || ldo < N || ldo > kMaxDim)
@@ -446,7 +446,17 @@ FP8FG_API int fp8_moe_mlp_few(const void* x, int in_dtype, int64_t T, int64_t K,
         return FP8_ERR_ALIGN;
     if (!device_is_sm100()) return FP8_ERR_DEVICE;
     return launch_moe_mlp_few(x, in_dtype, T, K, ldx, topk, weights, k, G, W13, s13, W2, s2, I, N, out,
-                              out_dtype, ldo, workspace, scale_mode, static_cast<cudaStream_t>(stream));
+                              out_dtype, ldo, workspace, scale_mode, static_cast<cudaStream_t>(stream), withhold);
+}
+
+FP8FG_API int fp8_moe_mlp_few(const void* x, int in_dtype, int64_t T, int64_t K, int64_t ldx,
+                              const int32_t* topk, const float* weights, int k, int G, const uint8_t* W13,
+                              const float* s13, const uint8_t* W2, const float* s2, int64_t I, int64_t N,
+                              void* out, int out_dtype, int64_t ldo, void* workspace,
+                              int64_t workspace_bytes, int scale_mode, void* stream)
+{
+    return moe_mlp_few(x, in_dtype, T, K, ldx, topk, weights, k, G, W13, s13, W2, s2, I, N, out, out_dtype, ldo,
+                       workspace, workspace_bytes, scale_mode, stream, 0);
 }
 
 FP8FG_API int fp8_get_status(void* stream)
@@ -506,6 +516,35 @@ FP8FG_API int fp8_selftest_gemm_unwind(int kernel, const uint8_t* A, const float
                        : launch_blockscaled_gemm_mx_withheld(A, sA, B, FP8_B_KMAJOR, sB, 128, M,
                                                              N, K, group_offsets, g, D, out_dtype,
                                                              N, st);
+}
+
+FP8FG_API int fp8_selftest_swiglu_bwd_unwind(const uint8_t* qh, const float* sh, const void* da, int in_dtype,
+                                             int64_t M, int64_t I, uint8_t* qdhT, float* sdhT, void* stream)
+{
+    if (!is_in(in_dtype)) return FP8_ERR_DTYPE;
+    if (M <= 0 || M > kMaxDim || M % 128 || I <= 0 || I > kMaxDim / 2 || I % 128 || (M + 15) / 16 > kMaxDim / (I / 128))
+        return FP8_ERR_SHAPE;
+    if (!qh || !sh || !da || !qdhT || !sdhT) return FP8_ERR_NULL;
+    if (!aligned(qh, 16) || !aligned(da, 16) || !aligned(qdhT, 16) || !aligned(sh, 4) || !aligned(sdhT, 4))
+        return FP8_ERR_ALIGN;
+    if (!device_is_sm100()) return FP8_ERR_DEVICE;
+    return launch_swiglu_bwd(qh, 2 * I, sh, da, in_dtype, I, M, I, nullptr, 0, nullptr, 0, nullptr, qdhT, M, sdhT,
+                             nullptr, 0, nullptr, nullptr, FP8_SCALE_FP32, static_cast<cudaStream_t>(stream),
+                             true) == cudaSuccess
+               ? FP8_OK
+               : FP8_ERR_LAUNCH;
+}
+
+FP8FG_API int fp8_selftest_moe_mlp_few_unwind(int phase, const void* x, int in_dtype, int64_t T, int64_t K,
+                                              const int32_t* topk, const float* weights, int k, int G,
+                                              const uint8_t* W13, const float* s13, const uint8_t* W2,
+                                              const float* s2, int64_t I, int64_t N, void* out, int out_dtype,
+                                              void* workspace, int64_t workspace_bytes, void* stream)
+{
+    if (phase != 1 && phase != 2) return FP8_ERR_DTYPE;
+    if (T <= 0) return FP8_ERR_SHAPE;
+    return moe_mlp_few(x, in_dtype, T, K, K, topk, weights, k, G, W13, s13, W2, s2, I, N, out, out_dtype, N,
+                       workspace, workspace_bytes, FP8_SCALE_FP32, stream, phase);
 }
 
 FP8FG_API int fp8_device_supported(void) { return device_is_sm100() ? 1 : 0; }

@@ -89,7 +89,8 @@ int launch_blockscaled_gemm_mx(const uint8_t* A, const float* sA, const uint8_t*
 // Read and clear that module's status word (caller synchronised).
 int read_and_clear_mx_status();
 
-// SwiGLU forward and backward around the FP8 checkpoint (swiglu.cu).
+// SwiGLU forward and backward around the FP8 checkpoint (swiglu.cu); `withhold` is the self-test of the
+// backward's failure path.
 cudaError_t launch_swiglu_quant(const void* h, int in_dtype, int64_t M, int64_t I, int64_t ldh,
                                 uint8_t* qa, int64_t ldqa, float* sa, uint8_t* qh, int64_t ldqh,
                                 float* sh, const int32_t* n_rows, int mode, cudaStream_t st);
@@ -97,17 +98,18 @@ cudaError_t launch_swiglu_bwd(const uint8_t* qh, int64_t ldqh, const float* sh, 
                               int in_dtype, int64_t ldda, int64_t M, int64_t I, void* dh, int64_t lddh,
                               uint8_t* qdh, int64_t ldqdh, float* sdh, uint8_t* qdhT, int64_t ldqdhT,
                               float* sdhT, uint8_t* qaT, int64_t ldqaT, float* saT,
-                              const int32_t* n_rows, int mode, cudaStream_t st);
+                              const int32_t* n_rows, int mode, cudaStream_t st, bool withhold = false);
 
 // Read and clear that module's status word (caller synchronised).
 int read_and_clear_swiglu_status();
 
-// The MoE MLP for few tokens (moe_few.cu); returns an fp8_status code.
+// The MoE MLP for few tokens (moe_few.cu); returns an fp8_status code.  `withhold` (1, 2) is the self-test of
+// that phase's failure path.
 int64_t moe_mlp_few_workspace_bytes(int64_t T, int k, int G, int64_t K, int64_t I, int64_t N);
 int launch_moe_mlp_few(const void* x, int in_dtype, int64_t T, int64_t K, int64_t ldx, const int32_t* topk,
                        const float* weights, int k, int G, const uint8_t* W13, const float* s13,
                        const uint8_t* W2, const float* s2, int64_t I, int64_t N, void* out, int out_dtype,
-                       int64_t ldo, void* workspace, int mode, cudaStream_t st);
+                       int64_t ldo, void* workspace, int mode, cudaStream_t st, int withhold = 0);
 // Read and clear that module's status word (caller synchronised).
 int read_and_clear_few_status();
 

@@ -104,6 +104,7 @@ struct Few {
     int64_t K, I, N;
     int T, Tp, k, G;        // Tp: T rounded up to 16, the row stride of per-token tables
     int out_dtype, mode;
+    int withhold;           // self-test: the phase (1, 2) whose CTAs never load their first unit's tokens
     uint64_t timeout_ns;
     // workspace
     int32_t* n_act;         // [1] number of active experts,
@@ -438,7 +439,7 @@ __device__ void few_producer(const CUtensorMap* tmW, const CUtensorMap* tmX, con
     };
     auto tokens = [&](const Walk<PHASE>& k, uint32_t it) {
         const int s = (int)(it % NS);
-        if (lane == 0) {
+        if (lane == 0 && (it > 0 || f.withhold != PHASE)) {
             tma_load_2d(smem + s * stage_bytes(NB) + W_BYTES, tmX, &sh.full[s],
                         (int32_t)((PHASE == 1 ? k.kb : k.j) * BK), PHASE == 1 ? 0 : (int32_t)(k.a * f.Tp));
             bulk_load(sh.tok[it % SLOTS], (PHASE == 1 ? f.xs : f.as) + (int64_t)k.kb * f.Tp, (uint32_t)f.Tp * 4,
@@ -1137,7 +1138,7 @@ int64_t moe_mlp_few_workspace_bytes(int64_t T, int k, int G, int64_t K, int64_t 
 int launch_moe_mlp_few(const void* x, int in_dtype, int64_t T, int64_t K, int64_t ldx, const int32_t* topk,
                        const float* weights, int k, int G, const uint8_t* W13, const float* s13,
                        const uint8_t* W2, const float* s2, int64_t I, int64_t N, void* out, int out_dtype,
-                       int64_t ldo, void* workspace, int mode, cudaStream_t st)
+                       int64_t ldo, void* workspace, int mode, cudaStream_t st, int withhold)
 {
     Few f;
     few_layout(&f, static_cast<uint8_t*>(workspace), T, k, G, K, I, N);
@@ -1156,6 +1157,7 @@ int launch_moe_mlp_few(const void* x, int in_dtype, int64_t T, int64_t K, int64_
     f.G = G;
     f.out_dtype = out_dtype;
     f.mode = mode;
+    f.withhold = withhold;
     f.timeout_ns = wait_timeout_ns();
     const int64_t A = T * k < G ? T * k : G;
     CUtensorMap tmW13, tmW2, tmX, tmA;

@@ -492,6 +492,23 @@ int fp8_selftest_gemm_unwind(int kernel, const uint8_t* A, const float* sA, cons
                              const float* sB, const int32_t* group_offsets, int G, int64_t M,
                              int64_t N, int64_t K, void* D, int out_dtype, void* stream);
 
+/*
+ * The same for the kernels of a gated MLP.  fp8_selftest_swiglu_bwd_unwind launches
+ * fp8_swiglu_bwd's kernel for outputs along tokens (qdhT [2I][M] alone; M % 128 == 0,
+ * contiguous operands, FP32 scales) with one warp of every CTA never handing over its part of the first
+ * tile; fp8_selftest_moe_mlp_few_unwind launches fp8_moe_mlp_few (contiguous operands,
+ * T >= 1) with every CTA of phase 1 or 2 holding back the token rows of its first unit. The waits
+ * run out, FP8_ERR_TIMEOUT is recorded, all roles and the kernels behind go on to their
+ * end, and the context stays usable; what the launch wrote is worthless.
+ */
+int fp8_selftest_swiglu_bwd_unwind(const uint8_t* qh, const float* sh, const void* da, int in_dtype, int64_t M,
+                                   int64_t I, uint8_t* qdhT, float* sdhT, void* stream);
+int fp8_selftest_moe_mlp_few_unwind(int phase, const void* x, int in_dtype, int64_t T, int64_t K,
+                                    const int32_t* topk, const float* weights, int k, int G,
+                                    const uint8_t* W13, const float* s13, const uint8_t* W2,
+                                    const float* s2, int64_t I, int64_t N, void* out, int out_dtype,
+                                    void* workspace, int64_t workspace_bytes, void* stream);
+
 /* 1 if the current device is an sm_100 GPU the library runs on, else 0. */
 int fp8_device_supported(void);
 
