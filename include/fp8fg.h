@@ -399,6 +399,9 @@ int fp8_swiglu_quant(const void* h, int in_dtype, int64_t M, int64_t I, int64_t 
  *   n_rows  as fp8_swiglu_quant.  In the 128x1 groups a row at or beyond it
  *           counts as zero (code 0 in a group with rows in use); whole groups
  *           beyond it, and rows of dh and qdh beyond it, are not written.
+ * Over the grouped rows of a dispatch, columns off[e] .. off[e+1] of qdhT and qaT, with
+ * those rows / 128 of their scales, are expert e's Wgrad operands; fp8_blockscaled_gemm
+ * (sb_gran 1) takes them once they are copied to rows of their own.
  * Sizes: M >= 0, and M % 128 == 0 when qdhT or qaT is wanted; I > 0,
  * I % 128 == 0, 2I <= 2^31 - 1; ldqh, lddh, ldqdh >= 2I, ldda >= I, ldqdhT,
  * ldqaT >= M.  One kernel launch.
