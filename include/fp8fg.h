@@ -371,10 +371,13 @@ int fp8_moe_combine(const void* D, int d_dtype, int64_t M_cap, int64_t N, const 
  *   n_rows  optional (NULL: M): number of rows in use, one int32 in DEVICE
  *        memory, e.g. group_offsets + G of a dispatch; clamped to [0, M].  Rows
  *        at or beyond it do not matter and are not written, nor are their scales.
- * silu and the products are FP32 and a is not rounded before its quantization.
+ * silu and the products are FP32 and a is not rounded before its quantization; for
+ * any gate, silu is within a few units in the last place, down to FP32's smallest
+ * normal number (g = -91.9), below which it may be less exact or zero.
  * Inputs are finite, and so is a; what is not spoils the 1x128 groups it lies in.
- * Sizes: M >= 0 (0 launches nothing), I > 0, I % 128 == 0, 2I <= 2^31 - 1;
- * ldh, ldqh >= 2I, ldqa >= I.  n_rows 4-byte aligned.  One kernel launch.
+ * Sizes: M >= 0 (0 launches nothing), I > 0, I % 128 == 0, 2I <= 2^31 - 1,
+ * ceil(M / 16) * (I / 128) <= 2^31 - 1; ldh, ldqh >= 2I, ldqa >= I.  n_rows
+ * 4-byte aligned.  One kernel launch.
  */
 int fp8_swiglu_quant(const void* h, int in_dtype, int64_t M, int64_t I, int64_t ldh, uint8_t* qa,
                      int64_t ldqa, float* sa, uint8_t* qh, int64_t ldqh, float* sh,
@@ -383,7 +386,8 @@ int fp8_swiglu_quant(const void* h, int in_dtype, int64_t M, int64_t I, int64_t 
 /*
  * Backward of that SwiGLU from the FP8 checkpoint alone ([P1] Figure 6: Dgrad
  * and Wgrad in FP8; [P2]/[P3]: per-token groups for Dgrad, groups along tokens
- * for Wgrad).  With g, u = code * scale of the checkpoint and s = 1/(1+exp(-g)):
+ * for Wgrad).  With g, u = code * scale of the checkpoint, FP32 products, and
+ * s = 1/(1+exp(-g)), as exact as the forward's silu:
  *   dG = dA * u * s * (1 + g * (1 - s)),  dU = dA * g * s,  dH = [dG | dU],
  *   a  = g * s * u  (recomputed)
  * Outputs, each one optional (NULL with its scales), at least one wanted:
@@ -403,8 +407,8 @@ int fp8_swiglu_quant(const void* h, int in_dtype, int64_t M, int64_t I, int64_t 
  * those rows / 128 of their scales, are expert e's Wgrad operands; fp8_blockscaled_gemm
  * (sb_gran 1) takes them once they are copied to rows of their own.
  * Sizes: M >= 0, and M % 128 == 0 when qdhT or qaT is wanted; I > 0,
- * I % 128 == 0, 2I <= 2^31 - 1; ldqh, lddh, ldqdh >= 2I, ldda >= I, ldqdhT,
- * ldqaT >= M.  One kernel launch.
+ * I % 128 == 0, 2I <= 2^31 - 1, ceil(M / 16) * (I / 128) <= 2^31 - 1;
+ * ldqh, lddh, ldqdh >= 2I, ldda >= I, ldqdhT, ldqaT >= M.  One kernel launch.
  */
 int fp8_swiglu_bwd(const uint8_t* qh, int64_t ldqh, const float* sh, const void* da, int in_dtype,
                    int64_t ldda, int64_t M, int64_t I, void* dh, int64_t lddh, uint8_t* qdh,
@@ -433,7 +437,11 @@ int fp8_swiglu_bwd(const uint8_t* qh, int64_t ldqh, const float* sh, const void*
  *   out     [T][ldo] BF16 or FP32 (out_dtype FP8_OUT_*)
  *   workspace  caller-owned device scratch of fp8_moe_mlp_few_workspace_bytes
  *           bytes, 256-byte aligned, contents on entry ignored; calls that may
- *           overlap (other streams, captured graphs that run at once) need one each
+ *           overlap (other streams, captured graphs that run at once) need one each.
+ *           It holds every active expert's sums and codes of all tokens, routed to it
+ *           or not: about min(T k, G) * I * (8 T + T') bytes, T' = T rounded up to 16
+ *           (128 tokens, top-8 of 32 experts of 7168 x 2048: 117 MB; of 256: 647 MB),
+ *           and 0.3 MB per token.
  * The sums are taken in a fixed order: equal inputs give equal bits.  What is not
  * finite stays with its token, or, in an expert's weights or scales, with the
  * tokens routed to that expert.
