@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 
 namespace fp8fg {
 
@@ -121,5 +122,20 @@ uint64_t wait_timeout_ns();
 void set_wait_timeout_ns(uint64_t ns);
 int device_sm_count();          // of the current device (cached per device)
 bool device_is_sm100();         // current device is compute capability 10.x
+
+// Once per kernel and device: opt into its dynamic shared memory.
+template <auto kernel>
+cudaError_t allow_smem(int bytes)
+{
+    static bool ready[64] = {};
+    static std::mutex mu;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lk(mu);
+    if (ready[dev]) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    ready[dev] = e == cudaSuccess;
+    return e;
+}
 
 }  // namespace fp8fg

@@ -41,7 +41,6 @@
 
 #include <cstddef>
 #include <cstdint>
-#include <mutex>
 
 #include "fp8fg_device.cuh"
 #include "fp8fg_host.h"
@@ -302,9 +301,9 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { tme
 template <int NB>
 struct __align__(16) FewShared {
     // A unit's scales arrive with its operands, in slot (unit number) % 8: the weight scale of
-    // each row block and the tokens' scales.  A slot is refilled 8 units later, when the ring
-    // (at most 6 stages) has been through the MMA of a unit that is at least 6 back, which
-    // waited for the promotion of the unit 2 before that: its readers are done.
+    // each row block and the tokens' scales.  A slot is refilled 8 units later, behind the MMA of the unit
+    // that had the ring's stage before: at most 6 back (the ring's depth), and itself behind the promotion of
+    // the unit 2 before it.  So the readers of a slot are done if NS + 2 <= SLOTS.
     float tok[SLOTS][NB];
     float wsc[SLOTS][2];
     uint64_t full[MAX_STAGES];
@@ -454,6 +453,8 @@ __device__ void few_producer(const CUtensorMap* tmW, const CUtensorMap* tmX, con
 #pragma unroll 1
     for (; n < NS && ahead.u < r.u1; ++n, ahead.next(r.u1)) weights(ahead, n);
     wait_previous();
+    // The kernels behind may start from this kernel's triggers on, and read what k_few_prep wrote (expert list,
+    // gate weights) before their own waits: no trigger may come before the wait above.
     bool triggered = false;
 #pragma unroll 1
     for (; k.u < r.u1; ++it, k.next(r.u1)) {
@@ -815,7 +816,7 @@ __global__ void __launch_bounds__(num_threads(NB), NB <= 16 ? 2 : 1)
 
 // Up to 32 tokens.  Block = (tile of phase 1, every gridDim.y-th 8 tokens): adds its parts for the tokens routed to its expert,
 // thread = channel; SwiGLU and 1x128 quantization.  Tokens not routed here (gate weight 0)
-// get zero rows of scale 0.  Everything but the parts is known (k_few_prep had completed before phase 1
+// get scale 0, for which phase 2 adds nothing, whatever their codes are.  Everything but the parts is known (k_few_prep had completed before phase 1
 // let this kernel start), and done, before phase 1 ends.
 constexpr int ACT_TOKENS = 8;
 
@@ -1073,27 +1074,13 @@ __global__ void __launch_bounds__(256) k_few_out_rows(const Few f, uint32_t ctas
 
 // ------------------------------------------------------------ host side
 
-template <auto kernel>
-bool few_allow_smem(int bytes)
-{
-    static bool ready[64] = {};
-    static std::mutex mu;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-    std::lock_guard<std::mutex> lk(mu);
-    if (!ready[dev])
-        ready[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
-                     cudaSuccess;
-    return ready[dev];
-}
-
 template <int NB>
 int launch_few_gemms(const Few& f, const CUtensorMap& tmW13, const CUtensorMap& tmW2, const CUtensorMap& tmX,
                      const CUtensorMap& tmA, unsigned ctas, cudaStream_t st)
 {
     constexpr uint32_t smem = num_stages(NB) * stage_bytes(NB) + (uint32_t)sizeof(FewShared<NB>);
     static_assert(smem <= (NB <= 16 ? 116736u - 1024u : 232448u), "shared memory of a CTA (two per SM up to 16 tokens)");
-    if (!few_allow_smem<k_few_gemm<1, NB>>((int)smem) || !few_allow_smem<k_few_gemm<2, NB>>((int)smem))
+    if (allow_smem<k_few_gemm<1, NB>>((int)smem) != cudaSuccess || allow_smem<k_few_gemm<2, NB>>((int)smem) != cudaSuccess)
         return FP8_ERR_LAUNCH;
     // both may start while the kernel before them in the stream still runs
     cudaLaunchAttribute attr[1];

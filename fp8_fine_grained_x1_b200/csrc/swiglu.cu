@@ -20,7 +20,6 @@
 
 #include <cstddef>
 #include <cstdint>
-#include <mutex>
 #include <type_traits>
 
 #include "fp8fg_device.cuh"
@@ -52,11 +51,6 @@ struct Quad;
 template <>
 struct Quad<__nv_bfloat16> {
     uint2 r;
-    __device__ __forceinline__ void zero() { r = make_uint2(0, 0); }
-    __device__ __forceinline__ void load_stream(const __nv_bfloat16* p)
-    {
-        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-    }
     __device__ __forceinline__ void load_shared(const void* p) { r = *static_cast<const uint2*>(p); }
     __device__ __forceinline__ void get(F2& a, F2& b) const
     {
@@ -67,8 +61,6 @@ struct Quad<__nv_bfloat16> {
 template <>
 struct Quad<float> {
     uint4 r;
-    __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void load_stream(const float* p) { r = ld_stream16(p); }
     __device__ __forceinline__ void load_shared(const void* p) { r = *static_cast<const uint4*>(p); }
     __device__ __forceinline__ void get(F2& a, F2& b) const
     {
@@ -738,21 +730,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_swiglu_bwd(const BwdParams p
             const int loads = (it - st + NST - 1) / NST;
             if (loads > 0) mbar_wait_drain(&s.full[st], (uint32_t)((loads - 1) & 1), p.timeout_ns);
         }
-}
-
-// Once per kernel and device: opt into its dynamic shared memory.
-template <auto kernel>
-cudaError_t allow_smem(int bytes)
-{
-    static bool ready[64] = {};
-    static std::mutex mu;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    std::lock_guard<std::mutex> lk(mu);
-    if (ready[dev]) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    ready[dev] = e == cudaSuccess;
-    return e;
 }
 
 template <typename Tin>
