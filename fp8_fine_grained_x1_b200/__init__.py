@@ -379,16 +379,32 @@ def _pair(a, b, what):
     return a is not None
 
 
+_queries = None
+
+
+def _current():
+    """(handle of a device's current stream, current device), as functions: torch's short forms (a call's host time can
+    outweigh its GPU time) where this torch has them, else its public ones."""
+    global _queries
+    if _queries is None:
+        import torch
+        _queries = (getattr(torch._C, "_cuda_getCurrentRawStream", None) or
+                    (lambda dev: torch.cuda.current_stream(dev).cuda_stream),
+                    getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device)
+    return _queries
+
+
 def _call_on(dev, stream, fn, where, *args):
     """fn(*args, stream) with device `dev` current, on its current stream unless one is given."""
     import torch
+    current_stream, current_device = _current()
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev)
+        raw = current_stream(dev)
     elif stream.device_index != dev:
         raise ValueError(f"{where}: stream of cuda:{stream.device_index}, tensors on cuda:{dev}")
     else:
         raw = stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
+    if current_device() == dev:
         code = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
