@@ -95,11 +95,12 @@ __device__ __forceinline__ uint32_t pack_bf16(F2 v)
 
 // ------------------------------------------------------------ forward
 
-// Threads of a CTA, rows per lane, and CTAs per SM (which caps the registers at 80).  BF16: of 1 to 4
-// rows and 64 to 256 threads these ran fastest over the range of sizes (4096 x 9216: 45.3 us, 135168 x
-// 2048: 305; 256 threads 46.8 and 315; 3 rows and 5 CTAs 45.5 and 300, but 3.8 us instead of 3.3 for
-// 1000 x 2048; others 47 to 54 and 315 to 358).  FP32 rows hold twice the registers: 16384 x 2048 takes
-// 57 us with one row, 69 with two, whose loads spill, 58 with two in 4 CTAs.
+// Threads of a CTA, rows per lane, and CTAs per SM (which caps the registers at 80; with a checkpoint 16 bytes
+// a thread spill).  BF16: 4096 x 9216 takes 46.4 us, 135168 x 2048 311.  Of 1 to 4 rows and 64 to 256
+// threads these ran fastest over the range of sizes, at 45.3 and 305 us before the sigmoid was as exact as it is:
+// 256 threads 46.8 and 315; 3 rows and 5 CTAs 45.5 and 300, but 3.8 us instead of 3.3 for
+// 1000 x 2048; others 47 to 54 and 315 to 358.  FP32 rows hold twice the registers: 16384 x 2048 takes
+// 58 us with one row, 69 with two, whose loads spill, 58 with two in 4 CTAs.
 constexpr int kFwdThreads = 128;
 constexpr int kFwdCtasPerSm = 6;
 template <typename T>
@@ -320,9 +321,9 @@ __device__ __forceinline__ void gradients(F2 g, F2 u, F2 da, F2& dg, F2& du, F2&
 __device__ __forceinline__ bool far_gates(float scale) { return !(fabsf(scale) <= kNearGates / 448.0f); }
 
 // Backward without transposed outputs: no group spans rows, so the work is split as the forward's (8
-// lanes own a row's channel block).  16384 x 2048, codes of dH alone: 35.7 us (FP32 dA 43.9), 46.6
-// (60.5) by the tiles of k_swiglu_bwd; 128 x 512 3.0 and 5.1.  Swept as the forward: 6 CTAs per SM 37.9
-// (49.0), 10 of one row 39.4 (44.6), 4 of three 41.3.
+// lanes own a row's channel block).  16384 x 2048, codes of dH alone: 37.9 us (FP32 dA 43.3), 46.6
+// (60.5) by the tiles of k_swiglu_bwd; 128 x 512 3.4 and 5.1.  With 7 CTAs per SM 38.3 (47.8), with 6 39.0 (50.4),
+// although 8 spill 48 bytes a thread of BF16; of other shapes, 10 CTAs of one row and 4 of three were 10 and 15 % slower.
 constexpr int kBwdRowsCtasPerSm = 8;
 template <typename Tda>
 __global__ void __launch_bounds__(kFwdThreads, kBwdRowsCtasPerSm) k_swiglu_bwd_rows(const BwdParams p)
@@ -462,9 +463,10 @@ __device__ __forceinline__ void cp_arrive(uint64_t* bar)
 // outT) is an mbarrier that a warp arrives on, does work that does not need it, and
 // then waits for -- the 1x128 groups get their scales and the rows of the tile before go out
 // between part and inv, the 1x128 groups are encoded between inv and outT.  (4096 x 9216 takes
-// 70.4 us; 71.1 with the 1x128 scales behind the channels', 75.5 with half of the 1x128 codes
-// before them.  Waits that suspend instead of spinning cost 2 % more; the checkpoint's scales
-// loaded into registers a tile ahead, 2 to 20 %, as the compiler lets them be waited for.)
+// 73.8 us.  Measured at 70.4, before the sigmoid was as exact as it is: 71.1 with the 1x128 scales behind the
+// channels', 75.5 with half of the 1x128 codes before them.  Waits that suspend instead of spinning cost 2 %
+// more; the checkpoint's scales loaded into registers a tile ahead, 2 to 20 %, as the compiler lets them be
+// waited for.)
 // Tokens at or beyond the rows in use count as zero in the 128x1 groups.
 // WITHHOLD (self-test): one warp never says that its part of the first tile's maxima is written.
 template <typename Tda, bool WITHHOLD = false>

@@ -33,6 +33,8 @@ grouping; gnrental.net post: BF16 or FP32 GEMM outputs.)
 
 Constructors allocate on torch's current stream: a step that is called on
 another stream has to be ordered behind it first, as its inputs have to be.
+A step's buffers are its own: its calls, and graphs captured from them, run one
+after the other.
 
 `kernel_calls` on each step counts the kernels one call launches.
 

@@ -373,7 +373,7 @@ int fp8_moe_combine(const void* D, int d_dtype, int64_t M_cap, int64_t N, const 
  *        at or beyond it do not matter and are not written, nor are their scales.
  * silu and the products are FP32 and a is not rounded before its quantization; for
  * any gate, silu is within a few units in the last place, down to FP32's smallest
- * normal number (g = -91.9), below which it may be less exact or zero.
+ * normal number (g >= -91.8), below which it may be less exact or zero.
  * Inputs are finite, and so is a; what is not spoils the 1x128 groups it lies in.
  * Sizes: M >= 0 (0 launches nothing), I > 0, I % 128 == 0, 2I <= 2^31 - 1,
  * ceil(M / 16) * (I / 128) <= 2^31 - 1; ldh, ldqh >= 2I, ldqa >= I.  n_rows
