@@ -92,20 +92,19 @@ __device__ __forceinline__ F2 sigmoid2(F2 g)
     return rcp_1p_exp(e, t, g);
 }
 
-// The sigmoid of any finite gates, as a product r * f: below about -86.6, r stays at 2^-125 and f is
+// The sigmoid of any gates, as a product r * f: below about -86.6, r stays at 2^-125 and f is
 // the rest, so that products with r first (g * r * f) are right down to FP32's smallest normal
-// number, where the sigmoid itself no longer is one; above, f is 1 and r has sigmoid2's bits. The
-// argument is kept where neither it nor what is made of it can overflow: the ends are 0 and 1.
+// number, where the sigmoid itself no longer is one; above, f is 1 and r has sigmoid2's bits.  Beyond
+// -340 and 138, where it is 0 and 1, the gate is taken for these: nothing overflows, not even an infinity.
 __device__ __forceinline__ void sigmoid2_far(F2 g, F2& r, F2& f)
 {
-    const F2 t = g * f2(-1.4426950408889634f, -1.4426950408889634f);
-    const float a = fminf(fmaxf(lo(t), -200.0f), 500.0f), b = fminf(fmaxf(hi(t), -200.0f), 500.0f);
-    const F2 e = f2(ex2_approx(fminf(a, 125.0f)), ex2_approx(fminf(b, 125.0f)));
-    r = rcp_1p_exp(e, f2(a, b), g);
-    f = f2(ex2_approx(fminf(125.0f - a, 0.0f)), ex2_approx(fminf(125.0f - b, 0.0f)));
+    const F2 c = f2(fminf(fmaxf(lo(g), -340.0f), 138.0f), fminf(fmaxf(hi(g), -340.0f), 138.0f));
+    const F2 t = c * f2(-1.4426950408889634f, -1.4426950408889634f);
+    r = rcp_1p_exp(f2(ex2_approx(fminf(lo(t), 125.0f)), ex2_approx(fminf(hi(t), 125.0f))), t, c);
+    f = f2(ex2_approx(fminf(125.0f - lo(t), 0.0f)), ex2_approx(fminf(125.0f - hi(t), 0.0f)));
 }
 
-// silu(g) = g * sigmoid(g); FAR for any finite gates, else for |g| <= kNearGates (with the same bits there).
+// silu(g) = g * sigmoid(g); FAR for any gates, else for |g| <= kNearGates (with the same bits there).
 template <bool FAR>
 __device__ __forceinline__ F2 silu2(F2 g)
 {

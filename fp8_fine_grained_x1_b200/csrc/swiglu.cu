@@ -95,7 +95,7 @@ __device__ __forceinline__ uint32_t pack_bf16(F2 v)
 
 // ------------------------------------------------------------ forward
 
-// Threads of a CTA, rows per lane, and CTAs per SM (which caps the registers at 80; with a checkpoint 16 bytes
+// Threads of a CTA, rows per lane, and CTAs per SM (which caps the registers at 80; with a checkpoint 8 bytes
 // a thread spill).  BF16: 4096 x 9216 takes 46.4 us, 135168 x 2048 311.  Of 1 to 4 rows and 64 to 256
 // threads these ran fastest over the range of sizes, at 45.3 and 305 us before the sigmoid was as exact as it is:
 // 256 threads 46.8 and 315; 3 rows and 5 CTAs 45.5 and 300, but 3.8 us instead of 3.3 for

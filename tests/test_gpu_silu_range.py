@@ -179,3 +179,22 @@ def test_few_tokens(T, mode):
     # POW2 scales: the activation's code is its value over a power of two, half an E4M3 step (2^-4) off
     tol = 1.4e-4 + (2.0 ** -4 if mode == fg.SCALE_POW2 else 0.0)
     assert np.all(np.abs(got - want) <= tol * np.abs(want))
+
+
+def test_infinite_gates():
+    """silu of +inf is +inf, of -inf and NaN NaN: the group's FP32 scale is infinite after the first, and its own
+    element a NaN code after all three."""
+    h = torch.ones((3, 256), device=dev())
+    h[:, 37] = torch.tensor([float("inf"), float("-inf"), float("nan")])
+    for dtype in (torch.float32, torch.bfloat16):
+        qa, sa, _, _ = fg.swiglu_quant(h.to(dtype))
+        assert bool(((qa[:, 37] & 0x7F) == 0x7F).all())
+        assert float(sa[0, 0]) == float("inf") and bool(torch.isfinite(sa[0, 1:]).all())
+    q = torch.full((128, 256), 0x38, dtype=torch.uint8, device=dev())
+    s = torch.ones((2, 128), device=dev())
+    s[0, 5] = float("inf")                                # all gates of a token
+    out = fg.swiglu_bwd(q, s, torch.ones((128, 128), device=dev()), ("dh", "qaT"))
+    assert bool(torch.isnan(out["dh"][5, :128]).all()) and bool((out["dh"][5, 128:] == float("inf")).all())
+    keep = torch.arange(128, device=dev()) != 5
+    assert bool(torch.isfinite(out["dh"][keep]).all())
+    assert bool((out["saT"] == float("inf")).all())
