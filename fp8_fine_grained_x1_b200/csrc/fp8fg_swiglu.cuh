@@ -74,8 +74,8 @@ __device__ __forceinline__ float rcp_approx(float x)
 // ln(2)'s rounding (2^-28.4 of it), and exp(-g) = 2^t * (1 + that) to FP32's precision.  The
 // exponential and the reciprocal are the hardware's approximations, at most two and one units in the last
 // place off.
-//
-// The reciprocal of 1 + e * (1 + what is lost).
+
+// The reciprocal of 1 + e * (1 + what is lost), e = 2^t.
 __device__ __forceinline__ F2 rcp_1p_exp(F2 e, F2 t, F2 g)
 {
     const F2 minus = f2(-1.0f, -1.0f), d = fma2(t, f2(0.6931471805599453f, 0.6931471805599453f), g);

@@ -334,8 +334,8 @@ class GatedMlpStep:
     H, A's codes and the operands of backward's GEMMs are scratch.  Each step
     has its own unless it is given another's: `share` is a step of the same sizes
     (another layer) whose scratch this one uses too, so that a model of many layers
-    holds it once (with hidden_dtype the same).  Steps that share run one after the other, in any order of
-    forward and backward passes."""
+    holds it once (with hidden_dtype the same).  Steps that share run one after the
+    other, in any order of forward and backward passes."""
     kernel_calls = 6             # x, w13, w2 quantizers, two GEMMs, the SwiGLU
     kernel_calls_backward = 8    # dy twice, cached x, the SwiGLU, four GEMMs
 
